@@ -22,3 +22,10 @@ from ._binding import (  # noqa: F401
     selftest_wait_timeout,
     version,
 )
+from ._paged import (  # noqa: F401
+    attn_paged_func,
+    attn_paged_fwd,
+    attn_paged_workspace_bytes,
+    paged_append_kv,
+    paged_slots,
+)

@@ -27,6 +27,16 @@ BLOCK = 128
 _lib = None
 
 
+class PagedCache(ctypes.Structure):
+    """b200attn_paged_cache of the header."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_page_stride", ctypes.c_int64), ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("v_page_stride", ctypes.c_int64), ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("Hkv", ctypes.c_int),
+                ("d_qk", ctypes.c_int), ("d_v", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
 class B200AttnError(RuntimeError):
     def __init__(self, code: int, what: str):
         msg = _lib.b200attn_strerror(code).decode() if _lib is not None else "library not loaded"
@@ -76,6 +86,14 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.b200attn_quantize_kv_workspace_bytes.argtypes = [i, i, i, i]
     lib.b200attn_quantize_kv_fp8.restype = i
     lib.b200attn_quantize_kv_fp8.argtypes = [vp] * 6 + [i] * 7 + [vp, sz, vp]
+    lib.b200attn_paged_slots.restype = i
+    lib.b200attn_paged_slots.argtypes = [vp, sz, i, vp, vp, i, i, i, vp, i] + [vp] * 7
+    lib.b200attn_paged_append.restype = i
+    lib.b200attn_paged_append.argtypes = [vp, vp, sz, sz, i, vp, vp, vp]
+    lib.b200attn_paged_fwd_workspace_bytes.restype = sz
+    lib.b200attn_paged_fwd_workspace_bytes.argtypes = [i, i, i, i]
+    lib.b200attn_paged_fwd.restype = i
+    lib.b200attn_paged_fwd.argtypes = [vp, sz, vp, vp, sz, i, vp, vp, i, i, i, i, i, f, vp, vp, vp, sz, vp]
     _lib = lib
     return lib
 

@@ -2,8 +2,9 @@
 
     python -m bf16_causal_prefill_fwd_b200.build [--force] [--verbose] [--trace]
 
-The library is a single translation unit (csrc/b200attn.cu) with the CUDA
-runtime linked statically, so it loads next to any PyTorch build.
+The library is two translation units (csrc/b200attn.cu and csrc/paged.cu),
+compiled side by side, with the CUDA runtime linked statically, so it loads
+next to any PyTorch build.
 """
 from __future__ import annotations
 
@@ -25,9 +26,10 @@ HEADER = os.path.join(ROOT, "include", "b200attn.h")
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",
     "-gencode", "arch=compute_100a,code=sm_100a",
-    "-Xcompiler", "-fPIC", "-shared", "-cudart", "static",
+    "-Xcompiler", "-fPIC", "-cudart", "static",
     "--expt-relaxed-constexpr",
 ]
+UNITS = ["b200attn.cu", "paged.cu"]
 
 
 def _nvcc() -> str:
@@ -38,7 +40,8 @@ def _nvcc() -> str:
 
 
 def sources() -> list[str]:
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh")) + [HEADER])
+    return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh"))
+                  + glob.glob(os.path.join(CSRC, "*.h")) + [HEADER])
 
 
 def up_to_date(path: str = LIB_PATH) -> bool:
@@ -56,18 +59,30 @@ def build(force: bool = False, verbose: bool = False, trace: bool = False) -> st
         return path
     os.makedirs(LIB_DIR, exist_ok=True)
     tmp = path + f".tmp{os.getpid()}"
-    cmd = [_nvcc(), *NVCC_FLAGS]
-    if trace:
-        cmd += ["-DATTN_TRACE"]
-    if verbose:
-        cmd += ["-Xptxas", "-v"]
-    cmd += ["-o", tmp, os.path.join(CSRC, "b200attn.cu")]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        sys.stderr.write(res.stdout + res.stderr)
+    objs, procs = [], []
+    try:
+        for unit in UNITS:
+            objs.append(f"{tmp}.{unit}.o")
+            cmd = [_nvcc(), *NVCC_FLAGS, "-c", "-o", objs[-1], os.path.join(CSRC, unit)]
+            if trace:
+                cmd += ["-DATTN_TRACE"]
+            if verbose:
+                cmd += ["-Xptxas", "-v"]
+            procs.append(subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True))
+        logs = [p.communicate()[0] for p in procs]
+        if all(p.returncode == 0 for p in procs):
+            link = subprocess.run([_nvcc(), *NVCC_FLAGS, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
+            logs.append(link.stdout + link.stderr)
+            procs.append(link)
+    finally:
+        for o in objs:
+            if os.path.exists(o):
+                os.remove(o)
+    failed = any(p.returncode != 0 for p in procs)
+    if failed or verbose:
+        sys.stderr.write("".join(logs))
+    if failed:
         raise RuntimeError(f"nvcc failed building {os.path.basename(path)}")
-    if verbose:
-        sys.stderr.write(res.stdout + res.stderr)
     os.replace(tmp, path)
     return path
 

@@ -17,6 +17,7 @@
 #include "attn_fwd_kernel.cuh"
 #include "attn_fwd_pair_kernel.cuh"
 #include "attn_fwd_tile_kernel.cuh"
+#include "paged_status.h"
 #include "quant_kernel.cuh"
 #include "varlen_units.cuh"
 
@@ -780,7 +781,8 @@ int b200attn_check(void* stream) {
   if (cudaMemcpyFromSymbol(&status, b200::g_b200attn_status, sizeof(int)) != cudaSuccess) return B200ATTN_ERR_CUDA;
   if (status != 0 && cudaMemcpyToSymbol(b200::g_b200attn_status, &zero, sizeof(int)) != cudaSuccess)
     return B200ATTN_ERR_CUDA;
-  return status;
+  const int paged = b200_paged_take_status();
+  return status != 0 ? status : paged;
 }
 
 const char* b200attn_strerror(int code) {
@@ -791,6 +793,7 @@ const char* b200attn_strerror(int code) {
     case B200ATTN_ERR_CUDA: return "CUDA runtime or driver error";
     case B200ATTN_ERR_TIMEOUT: return "a kernel gave up on a bounded wait";
     case B200ATTN_ERR_WORKSPACE: return "workspace missing or too small";
+    case B200ATTN_ERR_PAGES: return "the free list has too few pages";
     default: return "unknown status";
   }
 }

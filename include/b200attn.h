@@ -52,7 +52,8 @@ typedef enum {
   B200ATTN_ERR_UNSUPPORTED = -2, /* well-formed but not implemented (head dims, device) */
   B200ATTN_ERR_CUDA = -3,        /* the CUDA runtime or driver reported an error */
   B200ATTN_ERR_TIMEOUT = -4,     /* a kernel's bounded wait ran out (device status word) */
-  B200ATTN_ERR_WORKSPACE = -5    /* workspace missing or smaller than required */
+  B200ATTN_ERR_WORKSPACE = -5,   /* workspace missing or smaller than required */
+  B200ATTN_ERR_PAGES = -6        /* the free list has fewer pages than a step needs (device status word) */
 } b200attn_status;
 
 /* dtype of Q, K and V. */
@@ -336,9 +337,157 @@ int b200attn_quantize_fp8_static(const void* x, void* x_fp8, float* scale,
                                  int hadamard, void* stream);
 
 /*
+ * Serving from a paged key/value cache
+ * ------------------------------------
+ * Keys and values live in pages of page_size token rows; row j of a request's
+ * cache is row j % page_size of page block_table[b][j / page_size]. A serving
+ * step takes the requests' cached lengths and numbers of new tokens, and calls,
+ * in this order on one stream,
+ *   b200attn_paged_slots   lengths -> cu_seqlens, kv_lens, positions, slots (and
+ *                          new block-table entries off a free list),
+ *   b200attn_paged_append  the new K and V rows -> their slots,
+ *   b200attn_paged_fwd     attention of the new tokens over their requests' pages.
+ * There is no counterpart on the pages this library follows, which stop at
+ * prefill: these entry points carry its head shapes, head mapping, e4m3 codes
+ * with per-head scales and softmax conventions over to decoding and to prompts
+ * read in chunks.
+ *
+ * All lengths, tables and indices are read on the device only: the calls copy
+ * nothing, wait for nothing and can be captured into a graph and replayed on new
+ * contents. Contents that do not fit (see each entry point) leave the outputs
+ * they concern unwritten or empty, touch no memory outside the given tensors,
+ * and are reported by the next b200attn_check.
+ */
+
+/* A paged cache. Strides are in elements, multiples of 16 bytes; the d elements
+ * of a row are contiguous, so [pages, page_size, Hkv, d], [pages, Hkv, page_size,
+ * d] and K and V interleaved in one tensor are all described. */
+typedef struct {
+  void* k;  /* bf16, or e4m3 codes */
+  void* v;
+  int64_t k_page_stride, k_token_stride, k_head_stride;
+  int64_t v_page_stride, v_token_stride, v_head_stride;
+  int num_pages;  /* num_pages * page_size < 2^31 */
+  int page_size;  /* a multiple of 16 */
+  int Hkv;
+  int d_qk, d_v;  /* (128, 128) or (192, 128) */
+  int dtype;      /* B200ATTN_BF16 or B200ATTN_FP8_E4M3 */
+  const float* k_scale; /* e4m3: device fp32 [Hkv]; a code c stands for decode(c) * scale */
+  const float* v_scale;
+} b200attn_paged_cache;
+
+/*
+ * b200attn_paged_slots -- a step's bookkeeping, on the device.
+ *
+ * block_table   int32 [batch, table_width], rows table_stride apart; entry j of
+ *        row b is the page of rows [j * page_size, (j + 1) * page_size) of
+ *        request b. Entries of the cached tokens must be set; with free_pages
+ *        the entries the new tokens need are written, others never are.
+ * context_lens, new_lens  int32 [batch]: tokens cached / new in this step (each
+ *        may be 0); context_lens[b] + new_lens[b] <= table_width * page_size
+ * total  rows of positions and slots; the new tokens may be fewer (a padded
+ *        step): the rows behind them get position 0 and slot -1
+ * page_size  any size >= 1
+ * free_pages  optional int32 [free_count]: page numbers to take, in order, from
+ *        entry *free_head on; NULL: block_table is complete already
+ * free_head, free_head_out  int32 [1]: entries taken before / after the step.
+ *        They may be the same address.
+ * cu_seqlens  int32 [batch + 1] out: first new token of each request; the last
+ *        entry is the number of new tokens
+ * kv_lens     int32 [batch] out: context_lens + new_lens
+ * positions   int32 [total] out: position of each new token in its request
+ * slots       int32 [total] out: page * page_size + row of each new token
+ * batch <= 16384, total < 2^30.
+ *
+ * A step that does not fit (negative lengths, more than `total` new tokens, a
+ * request longer than its table row: INVALID; fewer free pages than needed:
+ * PAGES) is reported by b200attn_check and gives an empty step: cu_seqlens and
+ * kv_lens 0, every slot -1, the table unchanged, *free_head_out = *free_head.
+ * A negative table entry among those read gives its tokens slot -1 and INVALID.
+ *
+ * Errors: INVALID (NULL or misaligned pointers, sizes), UNSUPPORTED, CUDA.
+ */
+int b200attn_paged_slots(int* block_table, size_t table_stride, int table_width,
+                         const int* context_lens, const int* new_lens, int batch, int total, int page_size,
+                         const int* free_pages, int free_count, const int* free_head, int* free_head_out,
+                         int* cu_seqlens, int* kv_lens, int* positions, int* slots, void* stream);
+
+/*
+ * b200attn_paged_append -- writes K and V rows to their cache slots: bf16 as it
+ * is, or e4m3(x / scale[h]) rounded to nearest even and held at +-448 (NaN stays
+ * NaN).
+ *
+ * k, v   bf16 [total, Hkv, d_qk] and [total, Hkv, d_v]; tokens k_stride and
+ *        v_stride elements apart (multiples of 8), so that slices of one fused
+ *        projection's output can be given; a token's heads are contiguous
+ * slots  int32 [total]: cache row of each token; negative: the token is skipped;
+ *        num_pages * page_size or above: skipped and INVALID in the status word.
+ *        Slots of one call must differ (which of two rows with one slot stays is
+ *        not defined, and may differ between heads).
+ *
+ * Errors: INVALID, UNSUPPORTED (head dims, page_size, sizes), CUDA.
+ */
+int b200attn_paged_append(const void* k, const void* v, size_t k_stride, size_t v_stride, int total,
+                          const b200attn_paged_cache* cache, const int* slots, void* stream);
+
+/*
+ * b200attn_paged_fwd_workspace_bytes -- device workspace b200attn_paged_fwd
+ * needs, from sizes alone. Returns 0 for invalid sizes.
+ */
+size_t b200attn_paged_fwd_workspace_bytes(int total, int max_seqlen_q, int Hq, int Hkv);
+
+/*
+ * b200attn_paged_fwd -- attention of each request's new tokens over its cached
+ * keys and values, which include the new tokens' own (append first).
+ *
+ *     O[t,h,:] = softmax_j( s * Q[t,h,:] . K[j,h_k,:] ) V[j,h_k,:]
+ *
+ * over the keys j of t's request: with causal, new token i of nq sees keys
+ * j <= kv_len - nq + i; otherwise every j < kv_len. A row that sees no key gives
+ * O = 0 and lse = -inf.
+ *
+ * q      bf16 [total, Hq, d_qk], tokens q_stride elements apart (a multiple of
+ *        8), a token's heads contiguous; Hq / Hkv <= 128; query head h uses
+ *        key/value head h / (Hq / Hkv)
+ * cache  bf16: products in bf16, fp32 accumulation. e4m3: codes are taken as
+ *        fp16 exactly, Q and the probabilities as fp16 (Q after an exact power
+ *        of two per row), fp32 accumulation, per-head scales.
+ * block_table  int32 [batch, table_width], rows table_stride apart. Only the
+ *        entries of the first kv_lens[b] rows are read. An entry that is no page
+ *        reads as zero keys and values, and INVALID is reported.
+ * cu_seqlens  int32 [batch + 1]: new tokens [cu[b], cu[b+1]) belong to request b.
+ *        Rows of o and lse in no request (padding behind the last) stay as they
+ *        are.
+ * kv_lens  int32 [batch]: keys of each request, the new tokens' included
+ * total  rows of q and o
+ * max_seqlen_q  upper bound on the new tokens of any request, known on the host
+ *        (`total` if nothing better is); a request with more is skipped and
+ *        INVALID reported, like one whose cu_seqlens or kv_lens do not fit
+ * o      bf16 [total, Hq, d_v], contiguous
+ * lse    optional fp32 [Hq, total]
+ * softmax_scale  s; a value <= 0 selects 1/sqrt(d_qk)
+ * workspace  b200attn_paged_fwd_workspace_bytes bytes, 16-byte aligned, contents
+ *        on entry irrelevant; calls that may overlap (on different streams, in
+ *        different graphs) need distinct ones
+ *
+ * Cache rows at or behind kv_lens[b] are never part of a result, whatever they
+ * hold (NaN included). Results do not depend on timing: the same contents give
+ * the same bytes.
+ *
+ * Errors: INVALID, UNSUPPORTED (head dims, page_size not a multiple of 16,
+ * Hq / Hkv > 128, sizes past 32-bit counts), WORKSPACE, CUDA.
+ */
+int b200attn_paged_fwd(const void* q, size_t q_stride, const b200attn_paged_cache* cache,
+                       const int* block_table, size_t table_stride, int table_width,
+                       const int* cu_seqlens, const int* kv_lens, int batch, int total, int max_seqlen_q,
+                       int Hq, int causal, float softmax_scale, void* o, float* lse,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * b200attn_check -- synchronise `stream`, then return and clear the device
  * status word: 0, or B200ATTN_ERR_TIMEOUT if any kernel of this library gave
- * up on a wait since the last check; B200ATTN_ERR_CUDA if synchronising fails.
+ * up on a wait since the last check, or what a call found in its inputs on the
+ * device (INVALID, PAGES); B200ATTN_ERR_CUDA if synchronising fails.
  */
 int b200attn_check(void* stream);
 

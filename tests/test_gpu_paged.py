@@ -1,0 +1,257 @@
+"""The paged-cache operators on the GPU against their plain 64-bit forms."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import bf16_causal_prefill_fwd_b200 as b2
+from paged_reference import Paged, attention, check_attention, make
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = [(32, 8, 128), (16, 16, 192), (8, 1, 128), (28, 4, 128), (6, 2, 192), (16, 1, 128)]
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def run(p: Paged, **kw):
+    d = p.cuda()
+    got = b2.attn_paged_fwd(*d.args(), **d.scales(), return_lse=True, **kw)
+    assert b2.check() == 0
+    return got
+
+
+# ------------------------------------------------------------------------------------------- few rows (decoding)
+
+DECODE_LENS = [
+    ([1], [1]),
+    ([1, 1, 1, 1, 1, 1, 1, 1], [1, 15, 16, 17, 63, 64, 65, 1000]),
+    ([1, 0, 1, 0, 1], [300, 5, 0, 0, 129]),          # no new token; a token without keys
+    ([1] * 37, [1 + 53 * i for i in range(37)]),
+]
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("heads", SHAPES)
+@pytest.mark.parametrize("lens", DECODE_LENS)
+def test_decode_matches_the_plain_form(lens, heads, e4m3):
+    p = make(*lens, *heads, page_size=16, e4m3=e4m3, seed=len(lens[0]))
+    o, lse = run(p, max_seqlen_q=1)
+    check_attention(p, o, lse)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("page_size", [16, 32, 48, 64, 80, 128, 256])
+def test_decode_page_sizes(page_size, e4m3):
+    p = make([1, 1, 1], [page_size - 1, 3 * page_size + 5, 777], 8, 2, 128, page_size, e4m3, seed=page_size)
+    o, lse = run(p, max_seqlen_q=1)
+    check_attention(p, o, lse)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_few_new_tokens_of_one_request(e4m3, causal):
+    """Up to 16 rows per key/value head; requests with fewer keys than new tokens have rows that see nothing."""
+    p = make([4, 2, 3, 0, 4, 4], [200, 64, 2, 9, 0, 1], 8, 2, 128, 32, e4m3, seed=3)
+    o, lse = run(p, max_seqlen_q=4, causal=causal)
+    check_attention(p, o, lse, causal)
+    unseen = lse == -math.inf
+    assert bool((o.transpose(0, 1)[unseen] == 0).all())
+
+
+def test_decode_of_one_long_request_is_split_over_the_gpu():
+    p = make([1], [20011], 8, 2, 128, 16, seed=7)
+    o, lse = run(p, max_seqlen_q=1)
+    check_attention(p, o, lse)
+
+
+def test_decode_softmax_scale_and_large_scores():
+    p = make([1, 1], [500, 77], 8, 2, 128, 16, seed=8, spread=6.0)
+    o, lse = run(p, max_seqlen_q=1, softmax_scale=0.3)
+    check_attention(p, o, lse, softmax_scale=0.3)
+
+
+# ------------------------------------------------------------------------------------------- slots
+
+def plain_slots(table, ctx, new, total, ps, free=None, head=0):
+    table = [list(r) for r in table]
+    cu, kv, pos, slots = [0], [], [], []
+    for b, (c, n) in enumerate(zip(ctx, new)):
+        cu.append(cu[-1] + n)
+        kv.append(c + n)
+        if free is not None:
+            for j in range(-(-c // ps), -(-(c + n) // ps)):
+                table[b][j] = free[head]
+                head += 1
+        for x in range(c, c + n):
+            pos.append(x)
+            slots.append(table[b][x // ps] * ps + x % ps)
+    pad = total - len(pos)
+    return cu, kv, pos + [0] * pad, slots + [-1] * pad, table, head
+
+
+def slots_case(ctx, new, ps, pad, alloc, seed):
+    rng = np.random.default_rng(seed)
+    width = max(-(-(c + n) // ps) for c, n in zip(ctx, new)) + 1
+    pages = rng.permutation(len(ctx) * width + 50).tolist()
+    table = [[-1] * width for _ in ctx]
+    for b, (c, n) in enumerate(zip(ctx, new)):
+        for j in range(-(-(c if alloc else c + n) // ps)):
+            table[b][j] = pages.pop()
+    return table, (pages if alloc else None)
+
+
+@pytest.mark.parametrize("alloc", [False, True])
+@pytest.mark.parametrize("ps", [1, 7, 16, 64])
+@pytest.mark.parametrize("lens", [([0], [1]), ([5, 0, 16, 31, 100], [1, 0, 1, 17, 40]), ([3] * 700, [1] * 700),
+                                  ([i % 90 for i in range(2000)], [i % 4 for i in range(2000)]), ([0, 9], [0, 0])])
+def test_slots_match_the_plain_form(lens, ps, alloc):
+    ctx, new = lens
+    total = sum(new) + 13
+    table, free = slots_case(ctx, new, ps, 13, alloc, seed=ps)
+    want = plain_slots(table, ctx, new, total, ps, free, 2 if alloc else 0)
+    t = ints(table)
+    kw = dict(free_pages=ints(free), free_head=ints([2])) if alloc else {}
+    got = b2.paged_slots(t, ints(ctx), ints(new), total, ps, **kw)
+    assert b2.check() == 0
+    for g, w in zip(got[:4], want[:4]):
+        assert g.tolist() == w
+    assert t.tolist() == want[4]
+    if alloc:
+        assert got[4].tolist() == [want[5]]
+
+
+def test_slots_head_in_place_over_steps():
+    """Requests grow by steps, the head moving in place: no page is given out twice."""
+    ps, B = 16, 9
+    table, head = torch.full((B, 20), -1, dtype=torch.int32, device="cuda"), ints([0])
+    free = torch.randperm(200, dtype=torch.int32).cuda()
+    ctx = ints([0] * B)
+    for step in range(6):
+        new = ints([(7 * b + 11 * step) % 23 for b in range(B)])
+        cu, kv, pos, slots, out = b2.paged_slots(table, ctx, new, 250, ps, free_pages=free, free_head=head, free_head_out=head)
+        assert out is head
+        ctx = kv
+    assert b2.check() == 0
+    used = table[table >= 0].tolist()
+    assert len(used) == len(set(used)) == int(head)
+    assert [int((r >= 0).sum()) for r in table] == [-(-n // ps) for n in ctx.tolist()]
+
+
+@pytest.mark.parametrize("bad", ["negative_new", "negative_ctx", "total", "width", "both", "pages", "head"])
+def test_slots_that_do_not_fit_give_an_empty_step(bad):
+    ctx, new, total, free, head = [5, 20], [3, 4], 9, list(range(100, 110)), 1
+    code = -1
+    if bad == "negative_new":
+        new = [3, -1]
+    elif bad == "negative_ctx":
+        ctx = [-5, 20]
+    elif bad == "total":
+        total = 6
+    elif bad == "width":
+        new, total = [3, 45], 60
+    elif bad == "both":
+        head = 10      # pages of 4 rows: the second request's are more than a table row holds
+    elif bad == "pages":
+        new, total, head, code = [3, 13], 17, 10, -6
+    elif bad == "head":
+        head, code = -1, -6
+    table = ints([[1, -1, -1, -1], [2, 3, -1, -1]])
+    before = table.clone()
+    got = b2.paged_slots(table, ints(ctx), ints(new), total, 16 if bad != "both" else 4, free_pages=ints(free),
+                         free_head=ints([head]))
+    assert b2.check() == code
+    assert got[0].tolist() == [0, 0, 0] and got[1].tolist() == [0, 0]
+    assert got[3].tolist() == [-1] * total and got[4].tolist() == [head] and torch.equal(table, before)
+    assert b2.check() == 0
+
+
+def test_slots_of_an_unset_table_entry_are_reported():
+    got = b2.paged_slots(ints([[4, -1]]), ints([14]), ints([4]), 4, 16)
+    assert b2.check() == -1
+    assert got[3].tolist() == [4 * 16 + 14, 4 * 16 + 15, -1, -1]
+
+
+# ------------------------------------------------------------------------------------------- append
+
+def plain_codes(x, scale):
+    """e4m3(x / scale) from the division in fp32: clamp, then round to nearest even."""
+    y = (x.float() / scale[None, :, None]).clamp(-448.0, 448.0)
+    return y.to(torch.float8_e4m3fn)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("H,d_qk,T,ps", [(8, 128, 1, 16), (8, 128, 333, 16), (3, 192, 70, 48), (1, 128, 5, 16), (16, 192, 129, 64)])
+def test_append_matches_the_plain_form(H, d_qk, T, ps, e4m3):
+    g = torch.Generator().manual_seed(T)
+    pages = T // ps + 4
+    k, v = (torch.randn(T, H, d, generator=g).to(torch.bfloat16) for d in (d_qk, 128))
+    slots = torch.randperm(pages * ps, generator=g)[:T].to(torch.int32)
+    slots[T // 2] = -1  # a padded row
+    scales = [torch.rand(H, generator=g) * 0.01 + 0.004 for _ in range(2)]
+    dt = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    caches = [torch.randn(pages, ps, H, d, generator=g).to(dt) for d in (d_qk, 128)]
+    want = []
+    for x, c, s in zip((k, v), caches, scales):
+        w = c.clone().view(torch.uint8 if e4m3 else dt)
+        rows = w.view(pages * ps, H, -1)
+        y = plain_codes(x, s).view(torch.uint8) if e4m3 else x
+        keep = slots >= 0
+        rows[slots[keep].long()] = y[keep]
+        want.append(w)
+    got = [c.cuda() for c in caches]
+    kw = dict(k_scale=scales[0].cuda(), v_scale=scales[1].cuda()) if e4m3 else {}
+    b2.paged_append_kv(k.cuda(), v.cuda(), *got, slots.cuda(), **kw)
+    assert b2.check() == 0
+    for a, w in zip(got, want):
+        assert torch.equal(a.cpu().view(w.dtype), w)
+
+
+def test_append_of_special_values_into_e4m3():
+    x = torch.zeros(1, 1, 128, dtype=torch.bfloat16)
+    vals = [math.inf, -math.inf, math.nan, 1e30, -1e30, 448.0, 449.0, 464.0, 2.0 ** -9, 2.0 ** -10, 3 * 2.0 ** -11, -0.0]
+    x[0, 0, : len(vals)] = torch.tensor(vals)
+    kc, vc = (torch.zeros(1, 16, 1, 128, dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2))
+    one = torch.ones(1, device="cuda")
+    b2.paged_append_kv(x.cuda(), x.cuda(), kc, vc, ints([3]), k_scale=one, v_scale=one)
+    assert b2.check() == 0
+    got = kc[0, 3, 0, : len(vals)].float().cpu().tolist()
+    assert got[:2] == [448.0, -448.0] and math.isnan(got[2])
+    assert got[3:] == [448.0, -448.0, 448.0, 448.0, 448.0, 2.0 ** -9, 0.0, 2.0 ** -9, 0.0]
+    assert torch.equal(kc.view(torch.uint8), vc.view(torch.uint8))
+
+
+def test_append_slots_past_the_cache_are_skipped_and_reported():
+    kc, vc = (torch.zeros(2, 16, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    x = torch.ones(3, 2, 128, dtype=torch.bfloat16, device="cuda")
+    b2.paged_append_kv(x, x, kc, vc, ints([31, 32, 2 ** 31 - 1]))
+    assert b2.check() == -1
+    assert float(kc.sum()) == 256.0 and bool((kc[1, 15] == 1).all())
+
+
+# ------------------------------------------------------------------------------------------- layouts
+
+def test_strided_caches_and_slices_of_a_fused_projection():
+    """[pages, heads, rows, d] caches, K and V in one buffer, q, k and v slices of one tensor: the results of
+    contiguous copies, bit for bit."""
+    p = make([1, 1, 1], [40, 130, 333], 8, 2, 128, 16, seed=12).cuda()
+    ref = b2.attn_paged_fwd(*p.args(), max_seqlen_q=1)
+    P, ps, H, d = p.k_cache.shape
+    hnd = [c.permute(0, 2, 1, 3).contiguous().permute(0, 2, 1, 3) for c in (p.k_cache, p.v_cache)]
+    both = torch.stack([p.k_cache, p.v_cache], 1)
+    qkv = torch.cat([p.q.flatten(1), torch.zeros(3, 2 * H * d, dtype=torch.bfloat16, device="cuda")], 1)
+    q = qkv[:, : 8 * d].view(3, 8, d)
+    for kc, vc in (hnd, (both[:, 0], both[:, 1])):
+        assert not kc.is_contiguous()
+        got = b2.attn_paged_fwd(q, kc, vc, *p.args()[3:], max_seqlen_q=1)
+        assert torch.equal(got, ref)
+        k, v = (torch.randn(3, H, d, device="cuda").to(torch.bfloat16) for _ in range(2))
+        slots = ints([p.table[b, (n - 1) // ps].item() * ps + (n - 1) % ps for b, n in enumerate((40, 130, 333))])
+        a, c = kc.clone(), vc.contiguous().clone()
+        b2.paged_append_kv(k, v, kc, vc, slots)
+        b2.paged_append_kv(k, v, a, c, slots)
+        assert torch.equal(torch.nan_to_num(kc), torch.nan_to_num(a)) and torch.equal(torch.nan_to_num(vc), torch.nan_to_num(c))
+    assert b2.check() == 0
