@@ -10,6 +10,7 @@
 
 #include "../../include/b200attn.h"
 #include "paged_append.cuh"
+#include "paged_chunk.cuh"
 #include "paged_common.cuh"
 #include "paged_decode.cuh"
 #include "paged_slots.cuh"
@@ -146,6 +147,7 @@ template <int DQK, bool FP8, int NT>
 int launch_decode(const b200attn_paged_cache* c, PagedAttn p, int sm_count, cudaStream_t st) {
   using C = b200p::DecCfg<DQK, 128, FP8, NT>;
   p.box = gcd(p.page_size, b200p::kDecKeys);
+  p.slot_rows = b200p::kDecMaxRows;
   CUtensorMap tk, tv;
   if (!page_maps(&tk, &tv, c, p.box)) return B200ATTN_ERR_CUDA;
   auto kern = b200p::paged_decode_kernel<DQK, 128, FP8, NT>;
@@ -155,7 +157,7 @@ int launch_decode(const b200attn_paged_cache* c, PagedAttn p, int sm_count, cuda
   if (blocks > b200p::kDecMaxBlocks) blocks = b200p::kDecMaxBlocks;
   kern<<<blocks, b200p::kDecThreads, C::SMEM, st>>>(tk, tv, p);
   if (cudaGetLastError() != cudaSuccess) return B200ATTN_ERR_CUDA;
-  return launch_dependent(b200p::paged_join_kernel<128, b200p::kDecMaxRows>, dim3(blocks, 4, 1), 128, st,
+  return launch_dependent(b200p::paged_join_kernel<128>, dim3(blocks, 4, 1), 128, st,
                           static_cast<const PagedAttn>(p));
 }
 
@@ -163,6 +165,53 @@ template <int DQK, bool FP8>
 int launch_few(const b200attn_paged_cache* c, const PagedAttn& p, int sm_count, cudaStream_t st) {
   if (p.max_q * p.G <= 8) return launch_decode<DQK, FP8, 1>(c, p, sm_count, st);
   return launch_decode<DQK, FP8, 2>(c, p, sm_count, st);
+}
+
+// Rows of a workspace slot of the many-rows kernel.
+int chunk_rows(int total, int G) {
+  const int64_t rows = static_cast<int64_t>(total) * G;
+  return rows < b200p::kChRows ? static_cast<int>(rows) : b200p::kChRows;
+}
+
+template <int DQK, bool FP8>
+int launch_chunk(const b200attn_paged_cache* c, PagedAttn p, int sm_count, cudaStream_t st) {
+  using C = b200p::ChCfg<DQK, 128, FP8>;
+  p.box = gcd(p.page_size, b200p::kChN);
+  p.slot_rows = chunk_rows(p.T, p.G);
+  CUtensorMap tq = {}, tk = {}, tv = {};
+  b200p::ChCodes codes = {};
+  if (FP8) {
+    codes = {{static_cast<const uint8_t*>(c->k), static_cast<const uint8_t*>(c->v)},
+             {c->k_page_stride, c->v_page_stride},
+             {c->k_token_stride, c->v_token_stride},
+             {c->k_head_stride, c->v_head_stride}};
+  } else {
+    // {d, head, token} with a box of 64 columns, the G heads of a group and a tile's tokens
+    const cuuint64_t dims[3] = {DQK, (cuuint64_t)p.Hq, (cuuint64_t)p.T};
+    const cuuint64_t strides[2] = {DQK * 2, (cuuint64_t)(p.T > 1 ? p.q_stride : static_cast<int64_t>(p.Hq) * DQK) * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)(b200p::kChM / p.G)};
+    const cuuint32_t one[3] = {1, 1, 1};
+    EncodeTiledFn enc = encode_fn();
+    if (!enc || enc(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(p.q), dims, strides, box, one,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return B200ATTN_ERR_CUDA;
+    if (!page_maps(&tk, &tv, c, p.box)) return B200ATTN_ERR_CUDA;
+  }
+  auto kern = b200p::paged_chunk_kernel<DQK, 128, FP8>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+    return B200ATTN_ERR_CUDA;
+  // The role split (setmaxnreg) hands out registers from the block's launch
+  // allocation: a build with another count would wait for registers forever.
+  static const int regs = [&] {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, kern) == cudaSuccess ? a.numRegs : 0;
+  }();
+  if (regs != C::REGS_LAUNCH) return B200ATTN_ERR_UNSUPPORTED;
+  const int blocks = sm_count < b200p::kChMaxBlocks ? sm_count : b200p::kChMaxBlocks;
+  kern<<<blocks, C::THREADS, C::SMEM, st>>>(tq, tk, tv, p, codes);
+  if (cudaGetLastError() != cudaSuccess) return B200ATTN_ERR_CUDA;
+  return launch_dependent(b200p::paged_join_kernel<128>, dim3(blocks, 32, 1), 128, st, static_cast<const PagedAttn>(p));
 }
 
 }  // namespace
@@ -287,7 +336,7 @@ int b200attn_paged_append(const void* k, const void* v, size_t k_stride, size_t 
 size_t b200attn_paged_fwd_workspace_bytes(int total, int max_seqlen_q, int Hq, int Hkv) {
   if (total < 1 || max_seqlen_q < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return 0;
   if (few_rows(max_seqlen_q, Hq / Hkv)) return parts_of(b200p::kDecMaxBlocks, b200p::kDecMaxRows).bytes;
-  return 0;
+  return parts_of(b200p::kChMaxBlocks, chunk_rows(total, Hq / Hkv)).bytes;
 }
 
 int b200attn_paged_fwd(const void* q, size_t q_stride, const b200attn_paged_cache* cache, const int* block_table,
@@ -345,16 +394,24 @@ int b200attn_paged_fwd(const void* q, size_t q_stride, const b200attn_paged_cach
   p.lse = lse;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  if (few_rows(max_seqlen_q, G)) {
-    const Parts w = parts_of(b200p::kDecMaxBlocks, b200p::kDecMaxRows);
-    p.desc = reinterpret_cast<int*>(ws);
-    p.part_ml = reinterpret_cast<float*>(ws + w.ml);
-    p.part_o = reinterpret_cast<float*>(ws + w.o);
+  const bool few = few_rows(max_seqlen_q, G);
+  const Parts w = few ? parts_of(b200p::kDecMaxBlocks, b200p::kDecMaxRows)
+                      : parts_of(b200p::kChMaxBlocks, chunk_rows(total, G));
+  p.desc = reinterpret_cast<int*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + w.ml);
+  p.part_o = reinterpret_cast<float*>(ws + w.o);
+  if (few) {
     if (cache->d_qk == 128)
       return fp8 ? launch_few<128, true>(cache, p, sm_count, st) : launch_few<128, false>(cache, p, sm_count, st);
     return fp8 ? launch_few<192, true>(cache, p, sm_count, st) : launch_few<192, false>(cache, p, sm_count, st);
   }
-  return B200ATTN_ERR_UNSUPPORTED;
+  // key blocks of all units, counted in 32 bits
+  const int64_t pairs = static_cast<int64_t>(total) / (2 * (b200p::kChM / G)) + batch;
+  if (pairs * cache->Hkv >= (int64_t(1) << 31) || pairs * cache->Hkv * (keys / b200p::kChN + 1) >= (int64_t(1) << 31))
+    return B200ATTN_ERR_UNSUPPORTED;
+  if (cache->d_qk == 128)
+    return fp8 ? launch_chunk<128, true>(cache, p, sm_count, st) : launch_chunk<128, false>(cache, p, sm_count, st);
+  return fp8 ? launch_chunk<192, true>(cache, p, sm_count, st) : launch_chunk<192, false>(cache, p, sm_count, st);
 }
 
 }  // extern "C"

@@ -1,0 +1,771 @@
+// Attention of a chunk of new tokens over a paged cache: the many-rows half of
+// b200attn_paged_fwd (prompts read in pieces, drafted tokens, mixed steps).
+//
+//   O[r] = sum_j p_rj V_j / sum_j p_rj,  p_rj = 2^(c S_rj - m_r),  S = Q K^T
+//
+// on tcgen05, by the scheme of the prefill kernel: 128 x 128 score tiles into
+// tensor memory, one thread per row for the softmax, P back to tensor memory,
+// O accumulated there, two row tiles per block sharing each key block.
+//
+// Rows. The G query heads of a key/value head see the same keys, so a tile's
+// rows are (token, head) pairs: floor(128 / G) tokens times G heads. A chunk of
+// a few tokens then fills G times more rows of the tensor core's M = 128 than a
+// tile per head, and each key block is read once for all G heads. One TMA box
+// {64 columns, G heads, tokens} lays the rows out so.
+//
+// Split. A unit is (request, key/value head, pair of row tiles) and runs over
+// its key blocks of 128. The blocks of all units form one line that is cut into
+// equal runs, one per SM: a step of few units still uses every SM, and no SM
+// waits for a longer unit. A unit cut by a run's end leaves (m, l, O) per part,
+// joined in block order by paged_join_kernel. Every block finds its run from
+// the lengths in device memory.
+//
+// Keys and values. bf16: one warp copies K, one V, page piece by page piece
+// (TMA, 128-byte swizzle; pages behind the last are read as zeros through an
+// out-of-range page number). The rows behind the last key inside its page may
+// hold anything, and 0 * NaN is NaN, so the V warp clears them in shared memory
+// before the tensor core reads them; scores are replaced by select. e4m3: four
+// more warps read the codes (each 16-key group lies in one page), turn them into
+// fp16 exactly and write the swizzled tiles; they hold the next block's codes
+// in registers while they convert this one's, so the cache's latency is hidden.
+// Q then becomes fp16 too, after a power of two per row.
+//
+// Bound by the tensor core (2 x 2 x 128^3 products per key block and pair) and,
+// for chunks of a few tokens, by reading the cache.
+#pragma once
+
+#include "paged_common.cuh"
+
+namespace b200p {
+
+constexpr int kChM = 128;  // rows per tile
+constexpr int kChN = 128;  // keys per block
+constexpr int kChRows = 2 * kChM;
+constexpr int kChMaxBlocks = 160;  // workspace slots are sized for this many blocks
+
+template <int DQK, int DV, bool FP8>
+struct ChCfg {
+  static constexpr int THREADS = FP8 ? 512 : 384;
+  static constexpr int REGS_LAUNCH = FP8 ? 128 : 168;
+  // Register split by warpgroup: control, converters (e4m3), softmax. The sums
+  // stay within what the block was launched with.
+  static constexpr int REGS_CTRL = FP8 ? 56 : 72;
+  static constexpr int REGS_CONV = 104;
+  static constexpr int REGS_SOFT = FP8 ? 176 : 208;
+  static_assert(128 * REGS_CTRL + (FP8 ? 128 * REGS_CONV : 0) + 256 * REGS_SOFT <= THREADS * REGS_LAUNCH, "registers");
+  static constexpr int CHUNK = kChM * 128;  // 128 rows x 128 bytes, swizzled
+  static constexpr int QK_CHUNKS = DQK / 64, V_CHUNKS = DV / 64;
+  static constexpr int Q_BYTES = QK_CHUNKS * CHUNK, K_BYTES = QK_CHUNKS * CHUNK, V_BYTES = V_CHUNKS * CHUNK;
+  static constexpr int AVAIL = 227 * 1024 - 2048 - 2 * Q_BYTES;
+  static constexpr int PAIRS = AVAIL / (K_BYTES + V_BYTES);
+  static constexpr int SV = PAIRS >= 2 ? 2 : 1;
+  static constexpr int SK = (AVAIL - SV * V_BYTES) / K_BYTES > 3 ? 3 : (AVAIL - SV * V_BYTES) / K_BYTES;
+  static constexpr int BARS = 2 + 2 + 2 * SK + 2 * SV + 1 + 2 + 1 + 2 + 2 + 2 + 2 + 2;
+  static constexpr int SMEM = 2 * Q_BYTES + SK * K_BYTES + SV * V_BYTES + 1024 + 1024;
+  static_assert(8 * BARS + 64 <= 1024 && SMEM <= 227 * 1024 && SK >= 2, "shared memory");
+  // Tensor memory: S [0, 128) for both tiles in turn, O_t at 128 + 128 t, P_t
+  // (16-bit, 64 columns) at 384 + 64 t.
+  static constexpr int TM_O = 128, TM_P = 384;
+  // Operand format of kind::f16: 1 = bf16, 0 = fp16.
+  static constexpr uint32_t FMT = FP8 ? 0u : 1u;
+  static constexpr uint32_t IDESC_QK = idesc_dense(FMT, FMT, kChM, kChN, false);
+  static constexpr uint32_t IDESC_PV = idesc_dense(FMT, FMT, kChM, DV, true);
+  // How far (log2) the running maximum may lag behind the true one before O is
+  // rescaled: probabilities reach 2^T, which fp16 holds up to 2^15.
+  static constexpr float T_LAG = FP8 ? 8.0f : 16.0f;
+};
+
+// Key blocks of row tile `tile` of a request: 0 if the tile has no token; one
+// that masks everything for tokens that see no key.
+__device__ __forceinline__ int ch_blocks(const Request& r, int tile, int tpt, int causal) {
+  const int first = tile * tpt;
+  if (first >= r.nq) return 0;
+  const int seen = causal ? r.kv - r.nq + min(r.nq, first + tpt) : r.kv;
+  return max(1, (min(seen, r.kv) + kChN - 1) / kChN);
+}
+
+// Key blocks of pair `p`: its last tile that exists has most.
+__device__ __forceinline__ int ch_pair_blocks(const Request& r, int p, int tpt, int causal) {
+  return max(ch_blocks(r, 2 * p, tpt, causal), ch_blocks(r, 2 * p + 1, tpt, causal));
+}
+
+__device__ __forceinline__ int ch_pairs(const Request& r, int tpt) { return (r.nq + 2 * tpt - 1) / (2 * tpt); }
+
+// Key blocks of one key/value head of a request.
+__device__ __forceinline__ int ch_head_blocks(const Request& r, int tpt, int causal) {
+  const int n = ch_pairs(r, tpt);
+  if (n == 0) return 0;
+  if (!causal) return n * ch_pair_blocks(r, 0, tpt, causal);
+  int s = 0;
+  for (int p = 0; p < n; ++p) s += ch_pair_blocks(r, p, tpt, causal);
+  return s;
+}
+
+struct ChStart {
+  int b, h, pair, k0, count, first, per;
+};
+
+// A block's run of the line. Every thread of the block; `sm`: THREADS + 8 ints.
+template <int THREADS>
+__device__ __forceinline__ ChStart ch_start(const PagedAttn& p, int tpt, int* sm) {
+  const int tid = threadIdx.x;
+  const int seg = (p.B + THREADS - 1) / THREADS;
+  const int b0 = min(tid * seg, p.B), b1 = min(b0 + seg, p.B);
+  int sum = 0;
+  for (int b = b0; b < b1; ++b) sum += ch_head_blocks(paged_request(p, b, blockIdx.x == 0), tpt, p.causal);
+  sm[tid] = sum;
+  __syncthreads();
+  if (tid < 32) {
+    constexpr int per_lane = THREADS / 32;
+    int s = 0;
+    for (int i = 0; i < per_lane; ++i) s += sm[tid * per_lane + i];
+    int inc = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (tid >= o) inc += u;
+    }
+    int run = inc - s;
+    for (int i = 0; i < per_lane; ++i) {
+      const int v = sm[tid * per_lane + i];
+      sm[tid * per_lane + i] = run;
+      run += v;
+    }
+    if (tid == 31) sm[THREADS] = inc;
+  }
+  __syncthreads();
+  ChStart d;
+  const int total = sm[THREADS] * p.Hkv;
+  d.per = (total + gridDim.x - 1) / static_cast<int>(gridDim.x);
+  d.first = blockIdx.x * d.per;
+  d.count = max(0, min(d.per, total - d.first));
+  if (d.count > 0) {
+    int acc = sm[tid] * p.Hkv;
+    if (acc <= d.first && d.first < acc + sum * p.Hkv) {
+      for (int b = b0; b < b1; ++b) {
+        const Request r = paged_request(p, b, false);
+        const int n = ch_head_blocks(r, tpt, p.causal);
+        if (d.first < acc + n * p.Hkv) {
+          int at = (d.first - acc) % n, pair = 0;
+          for (int m; at >= (m = ch_pair_blocks(r, pair, tpt, p.causal)); ++pair) at -= m;
+          sm[THREADS + 1] = b;
+          sm[THREADS + 2] = (d.first - acc) / n;
+          sm[THREADS + 3] = pair;
+          sm[THREADS + 4] = at;
+          break;
+        }
+        acc += n * p.Hkv;
+      }
+    }
+  }
+  __syncthreads();
+  d.b = sm[THREADS + 1];
+  d.h = sm[THREADS + 2];
+  d.pair = sm[THREADS + 3];
+  d.k0 = sm[THREADS + 4];
+  return d;
+}
+
+// Walks the pieces of a block's run: key blocks [kb, ke) of unit (b, h, pair).
+struct ChWalk {
+  const PagedAttn& p;
+  Request r;
+  int b, h, pair, tpt;
+  int kb, ke, n0, n1;  // this piece; key blocks of the unit's tiles
+  int left, at;        // blocks after this piece; the piece's place in the line
+  __device__ ChWalk(const PagedAttn& params, const ChStart& d, int tokens) : p(params), tpt(tokens) {
+    b = d.b;
+    h = d.h;
+    pair = d.pair;
+    left = d.count;
+    at = d.first;
+    kb = d.k0;
+    ke = kb;
+    if (left > 0) {
+      r = paged_request(p, b, false);
+      take();
+    }
+  }
+  __device__ void take() {
+    n0 = ch_blocks(r, 2 * pair, tpt, p.causal);
+    n1 = ch_blocks(r, 2 * pair + 1, tpt, p.causal);
+    const int n = min(left, max(n0, n1) - kb);
+    ke = kb + n;
+    left -= n;
+  }
+  __device__ bool valid() const { return ke > kb; }
+  __device__ int end(int t) const { return min(ke, t ? n1 : n0); }      // tile t runs blocks [kb, end(t))
+  __device__ bool has(int t) const { return end(t) > kb; }
+  __device__ bool whole() const { return kb == 0 && ke == max(n0, n1); }
+  __device__ void next() {
+    at += ke - kb;
+    kb = ke = 0;
+    if (left == 0) return;
+    if (++pair == ch_pairs(r, tpt)) {
+      pair = 0;
+      if (++h == p.Hkv) {
+        h = 0;
+        do {  // more blocks are left, so a request with tokens follows
+          if (++b >= p.B) {
+            left = 0;
+            return;
+          }
+          r = paged_request(p, b, false);
+        } while (r.nq == 0);
+      }
+    }
+    take();
+  }
+};
+
+// 2^x for two lanes on the FMA pipe (Cody-Waite split, degree-3 polynomial of
+// relative error 2.2e-4 on [-1/2, 1/2]); below -125: 0.
+__device__ __forceinline__ void ch_exp2_fma(float x0, float x1, float& r0, float& r1) {
+  constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
+  const float a0 = fmaxf(x0, -125.0f), a1 = fmaxf(x1, -125.0f);
+  float j0, j1, n0, n1, f0, f1, p0, p1;
+  ffma2_bcast(a0, a1, 1.0f, kRound, j0, j1);
+  ffma2_bcast(j0, j1, 1.0f, -kRound, n0, n1);
+  ffma2(n0, n1, -1.0f, -1.0f, a0, a1, f0, f1);
+  ffma2_bcast(f0, f1, 0.05286737531423569f, 0.24215202033519745f, p0, p1);
+  ffma2(p0, p1, f0, f1, 0.6935867667198181f, 0.6935867667198181f, p0, p1);
+  ffma2(p0, p1, f0, f1, 0.9999627470970154f, 0.9999627470970154f, p0, p1);
+  r0 = x0 >= -125.0f ? __uint_as_float(__float_as_uint(p0) + (__float_as_uint(j0) << 23)) : 0.0f;
+  r1 = x1 >= -125.0f ? __uint_as_float(__float_as_uint(p1) + (__float_as_uint(j1) << 23)) : 0.0f;
+}
+
+// Largest of three; NaN if one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// e4m3 caches: what the converting warps read codes from (strides in bytes).
+struct ChCodes {
+  const uint8_t* base[2];
+  int64_t page[2], token[2], head[2];
+};
+
+// One block of 128 keys of K or V as codes in registers: thread `tid` of 128
+// holds, of each 32 keys, units tid, tid + 128, ... (16 codes each, D / 16 to a row).
+template <int D>
+struct ChRegs {
+  static constexpr int UPR = D / 16, PER = 32 * UPR / 128;
+  uint4 c[4][PER];
+  __device__ __forceinline__ void load(const ChCodes& s, int which, int h, int kv0, int kv, int pages, int ps,
+                                       int num_pages, int tid) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int idx = i * 128 + tid, row = idx / UPR, u = idx - row * UPR;
+        const int key = kv0 + 32 * g + row;
+        const int page = __shfl_sync(0xffffffffu, pages, 2 * g + (row >> 4));
+        c[g][i] = make_uint4(0, 0, 0, 0);
+        if (key < kv && page < num_pages)
+          c[g][i] = __ldg(reinterpret_cast<const uint4*>(s.base[which] + page * s.page[which] +
+                                                         (key % ps) * s.token[which] + h * s.head[which] + u * 16));
+      }
+  }
+  __device__ __forceinline__ void store(uint32_t dst, int tid) const {
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int idx = i * 128 + tid, r32 = idx / UPR, u = idx - r32 * UPR, row = 32 * g + r32;
+        const uint4 v = c[g][i];
+        const uint32_t line = dst + (u >> 2) * (kChN * 128) + row * 128;
+        const uint32_t a[2][4] = {{e4m3x2_f16x2(v.x), e4m3x2_f16x2(v.x >> 16), e4m3x2_f16x2(v.y), e4m3x2_f16x2(v.y >> 16)},
+                                  {e4m3x2_f16x2(v.z), e4m3x2_f16x2(v.z >> 16), e4m3x2_f16x2(v.w), e4m3x2_f16x2(v.w >> 16)}};
+        // units of the even and odd column blocks go out in opposite order, so
+        // that eight lanes of a row hit all eight 16-byte banks
+        const bool odd = (u >> 2) & 1;
+        const int u0 = 2 * (u & 3) + (odd ? 1 : 0), u1 = u0 ^ 1;
+        st_shared_v4(line + ((u0 ^ (row & 7)) << 4), odd ? a[1][0] : a[0][0], odd ? a[1][1] : a[0][1],
+                     odd ? a[1][2] : a[0][2], odd ? a[1][3] : a[0][3]);
+        st_shared_v4(line + ((u1 ^ (row & 7)) << 4), odd ? a[0][0] : a[1][0], odd ? a[0][1] : a[1][1],
+                     odd ? a[0][2] : a[1][2], odd ? a[0][3] : a[1][3]);
+      }
+  }
+};
+
+template <int DQK, int DV, bool FP8>
+__global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
+    paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, const PagedAttn p, const ChCodes codes) {
+  using C = ChCfg<DQK, DV, FP8>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t* gen = smem_raw + (base - raw);
+  const uint32_t sQ = base, sK = sQ + 2 * C::Q_BYTES, sV = sK + C::SK * C::K_BYTES, sBar = sV + C::SV * C::V_BYTES;
+  uint8_t* bar_gen = gen + (sBar - base);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_gen + 8 * C::BARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bar_gen + 8 * C::BARS + 4);
+
+  const uint32_t bQFull = sBar;                  // [2] Q tile there (TMA, or 128 softmax threads)
+  const uint32_t bQEmpty = bQFull + 16;          // [2] the tile's last QK^T has read it
+  const uint32_t bKFull = bQEmpty + 16;          // [SK]
+  const uint32_t bKEmpty = bKFull + 8 * C::SK;   // [SK]
+  const uint32_t bVFull = bKEmpty + 8 * C::SK;   // [SV]
+  const uint32_t bVEmpty = bVFull + 8 * C::SV;   // [SV]
+  const uint32_t bVTail = bVEmpty + 8 * C::SV;   // a V block whose last rows must be cleared
+  const uint32_t bSFull = bVTail + 8;            // [2]
+  const uint32_t bSFree = bSFull + 16;           // [1] the S buffer has been copied out
+  const uint32_t bPFull = bSFree + 8;            // [2]
+  const uint32_t bPDone = bPFull + 16;           // [2]
+  const uint32_t bOFull = bPDone + 16;           // [2]
+  const uint32_t bOEmpty = bOFull + 16;          // [2]
+  const uint32_t bDrain = bOEmpty + 16;          // [2]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tpt = kChM / p.G;  // tokens per tile
+
+  pdl_launch_dependents();
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int t = 0; t < 2; ++t) {
+        mbar_init(bQFull + 8 * t, FP8 ? 128 : 1);
+        mbar_init(bQEmpty + 8 * t, 1);
+        mbar_init(bSFull + 8 * t, 1);
+        mbar_init(bPFull + 8 * t, 128);
+        mbar_init(bPDone + 8 * t, 1);
+        mbar_init(bOFull + 8 * t, 1);
+        mbar_init(bOEmpty + 8 * t, 128);
+        mbar_init(bDrain + 8 * t, 1);
+      }
+      mbar_init(bSFree, 128);
+      mbar_init(bVTail, 1);
+      for (int s = 0; s < C::SK; ++s) {
+        mbar_init(bKFull + 8 * s, FP8 ? 128 : 1);
+        mbar_init(bKEmpty + 8 * s, 1);
+      }
+      for (int s = 0; s < C::SV; ++s) {
+        mbar_init(bVFull + 8 * s, FP8 ? 128 : 1);
+        mbar_init(bVEmpty + 8 * s, 1);
+      }
+      *abort_flag = 0;
+      fence_mbar_init();
+      if constexpr (!FP8) {
+        prefetch_tmap(&tmQ);
+        prefetch_tmap(&tmK);
+        prefetch_tmap(&tmV);
+      }
+    }
+    __syncwarp();
+    tmem_alloc(smem_addr(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  const ChStart d = ch_start<C::THREADS>(p, tpt, reinterpret_cast<int*>(gen));  // in the Q buffers, not in use yet
+  fence_proxy_async_smem();  // TMA writes there next
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (threadIdx.x == 0) reinterpret_cast<PartDesc*>(p.desc)[blockIdx.x].last = -1;
+
+  if (warp < 4) {
+    setmaxnreg_dec<C::REGS_CTRL>();
+    if (warp == 0 || warp == 3) {
+      // ---------------------------------------------------------- copies (bf16 caches)
+      if constexpr (!FP8) {
+        const bool is_k = warp == 0;
+        const int nslot = is_k ? C::SK : C::SV;
+        const uint32_t ring = is_k ? sK : sV, slot_bytes = is_k ? C::K_BYTES : C::V_BYTES;
+        const uint32_t bFull = is_k ? bKFull : bVFull, bEmpty = is_k ? bKEmpty : bVEmpty;
+        const CUtensorMap* tm = is_k ? &tmK : &tmV;
+        const int chunks = is_k ? C::QK_CHUNKS : C::V_CHUNKS;
+        const int boxes = kChN / p.box, issues = boxes * chunks, ahead = 32 / boxes;
+        const int box = lane / chunks, c = lane - box * chunks;
+        const uint32_t q_bytes = C::QK_CHUNKS * 128 * tpt * p.G;
+        uint32_t it = 0, tails = 0, nq[2] = {0, 0};
+        bool ok = true;
+        for (ChWalk w(p, d, tpt); ok && w.valid(); w.next()) {
+          if (is_k) {
+            for (int t = 0; t < 2 && ok; ++t) {
+              if (!w.has(t)) continue;
+              if (nq[t] > 0) ok = __all_sync(0xffffffffu, paged_wait(bQEmpty + 8 * t, (nq[t] - 1) & 1, abort_flag));
+              if (!ok) break;
+              ++nq[t];
+              if (lane == 0) {
+                mbar_arrive_expect_tx(bQFull + 8 * t, q_bytes);
+                for (int i = 0; i < C::QK_CHUNKS; ++i)
+                  tma_load_3d(sQ + t * C::Q_BYTES + i * C::CHUNK, &tmQ, bQFull + 8 * t, i * 64, w.h * p.G,
+                              w.r.t0 + (2 * w.pair + t) * tpt);
+              }
+            }
+          }
+          int page = 0;
+          for (int j = w.kb; j < w.ke && ok; ++j, ++it) {
+            const int a = (j - w.kb) % ahead;
+            if (a == 0) page = lane < ahead * boxes ? paged_page(p, w.b, j * kChN + lane * p.box, w.r.kv) : 0;
+            const uint32_t s = it % nslot;
+            if (it >= static_cast<uint32_t>(nslot))
+              ok = __all_sync(0xffffffffu, paged_wait(bEmpty + 8 * s, ((it / nslot) - 1) & 1, abort_flag));
+            if (!ok) break;
+            const bool tail = !is_k && (j + 1) * kChN > w.r.kv;
+            const uint32_t bar = tail ? bVTail : bFull + 8 * s;
+            if (lane == 0) mbar_arrive_expect_tx(bar, slot_bytes);
+            __syncwarp();
+            const int pg = __shfl_sync(0xffffffffu, page, a * boxes + (lane < issues ? box : 0));
+            if (lane < issues)
+              tma_load_4d(ring + s * slot_bytes + c * C::CHUNK + box * p.box * 128, tm, bar, c * 64, w.h,
+                          (j * kChN + box * p.box) % p.page_size, pg);
+            if (tail) {
+              ok = __all_sync(0xffffffffu, paged_wait(bVTail, tails & 1, abort_flag));
+              ++tails;
+              const int from = max(0, w.r.kv - j * kChN);
+              for (int i = lane; i < (kChN - from) * C::V_CHUNKS * 8; i += 32) {
+                const int row = from + i / (C::V_CHUNKS * 8), cc = (i / 8) % C::V_CHUNKS;
+                st_shared_v4(ring + s * slot_bytes + cc * C::CHUNK + row * 128 + 16 * (i & 7), 0u, 0u, 0u, 0u);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bFull + 8 * s);
+            }
+          }
+        }
+        if (!ok) __nanosleep(200000);  // copies in flight land before the block ends
+      }
+      __syncwarp();
+    } else {
+      // ---------------------------------------------------------- MMA issuers: warp 1 S = Q K^T, warp 2 O += P V
+      if (lane == 0) {
+        const uint32_t q_lo0 = sdesc_lo(sQ, 16), k_lo0 = sdesc_lo(sK, 16), v_lo0 = sdesc_lo(sV, C::CHUNK);
+        uint32_t it = 0, ns = 0, cnt[2] = {0, 0}, g[2] = {0, 0};
+        bool ok = true;
+        for (ChWalk w(p, d, tpt); ok && w.valid(); w.next()) {
+          if (warp == 1) {
+            for (int t = 0; t < 2 && ok; ++t)
+              if (w.has(t)) ok = paged_wait(bQFull + 8 * t, cnt[t]++ & 1, abort_flag);
+            for (int j = w.kb; j < w.ke && ok; ++j, ++it) {
+              const uint32_t s = it % C::SK;
+              if (!(ok = paged_wait(bKFull + 8 * s, (it / C::SK) & 1, abort_flag))) break;
+              for (int t = 0; t < 2; ++t) {
+                const int e = w.end(t);
+                if (j >= e) continue;
+                if (ns > 0 && !(ok = paged_wait(bSFree, (ns - 1) & 1, abort_flag))) break;
+                ++ns;
+                tc_fence_after();
+                const uint32_t a_lo = q_lo0 + t * (C::Q_BYTES >> 4), b_lo = k_lo0 + s * (C::K_BYTES >> 4);
+#pragma unroll
+                for (int kk = 0; kk < DQK / 16; ++kk) {
+                  const uint32_t off = ((kk / 4) * C::CHUNK + (kk % 4) * 32) >> 4;
+                  mma_ss_lo<false>(tmem, a_lo + off, b_lo + off, C::IDESC_QK, kk > 0 ? 1u : 0u);
+                }
+                tc_commit(bSFull + 8 * t);
+                if (j == e - 1) tc_commit(bQEmpty + 8 * t);
+              }
+              if (!ok) break;
+              tc_commit(bKEmpty + 8 * s);
+            }
+          } else {
+            for (int j = w.kb; j < w.ke && ok; ++j, ++it) {
+              const uint32_t s = it % C::SV;
+              if (!(ok = paged_wait(bVFull + 8 * s, (it / C::SV) & 1, abort_flag))) break;
+              for (int t = 0; t < 2; ++t) {
+                const int e = w.end(t);
+                if (j >= e) continue;
+                if (!(ok = paged_wait(bPFull + 8 * t, g[t]++ & 1, abort_flag))) break;
+                if (j == w.kb) {
+                  if (cnt[t] > 0 && !(ok = paged_wait(bOEmpty + 8 * t, (cnt[t] - 1) & 1, abort_flag))) break;
+                  ++cnt[t];
+                }
+                tc_fence_after();
+                const uint32_t o = tmem + C::TM_O + 128 * t, a = tmem + C::TM_P + 64 * t;
+                const uint32_t b_lo = v_lo0 + s * (C::V_BYTES >> 4);
+#pragma unroll
+                for (int kk = 0; kk < kChN / 16; ++kk)
+                  mma_ts_lo<false>(o, a + 8 * kk, b_lo + ((kk * 16 * 128) >> 4), C::IDESC_PV,
+                                   kk > 0 || j > w.kb ? 1u : 0u);
+                tc_commit(bPDone + 8 * t);
+                if (j == e - 1) tc_commit(bOFull + 8 * t);
+              }
+              if (!ok) break;
+              tc_commit(bVEmpty + 8 * s);
+            }
+          }
+        }
+        // every MMA this thread issued has completed before the block frees its tensor memory
+        const uint32_t drain = bDrain + 8 * (warp - 1);
+        tc_commit(drain);
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_try_wait(drain, 0) && global_timer_ns() - t0 < kPagedWaitLimitNs) {
+        }
+      }
+      __syncwarp();
+    }
+  } else if (warp < 12) {
+    setmaxnreg_inc<C::REGS_SOFT>();
+    // ------------------------------------------------------------ softmax and epilogue, one thread per row
+    const int t = (warp - 4) >> 2;
+    const int r = threadIdx.x - 128 - 128 * t;
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t tS = tmem + lanes, tO = tmem + lanes + C::TM_O + 128 * t, tP = tmem + lanes + C::TM_P + 64 * t;
+    const int rtok = r / p.G, rhead = r - rtok * p.G;
+    uint32_t g = 0, units = 0;  // key blocks and pieces this tile has done
+    bool ok = true;
+    for (ChWalk w(p, d, tpt); ok && w.valid(); w.next()) {
+      const int tok = (2 * w.pair + t) * tpt + rtok;
+      const bool real = rtok < tpt && tok < w.r.nq;
+      const bool whole = w.whole(), head = w.kb > 0;
+      const int slot = 2 * blockIdx.x + (head ? 0 : 1);
+      const int64_t part = static_cast<int64_t>(slot) * p.slot_rows + t * tpt * p.G + r;
+      if (t == 0 && r == 0 && !whole && !head) {
+        PartDesc e;
+        e.last = (w.at + max(w.n0, w.n1) - 1) / d.per;
+        e.t0 = w.r.t0;
+        e.row0 = 2 * w.pair * tpt * p.G;
+        e.nrows = min(2 * tpt, w.r.nq - 2 * w.pair * tpt) * p.G;
+        e.hkv = w.h;
+        e.pad[0] = e.pad[1] = e.pad[2] = 0;
+        reinterpret_cast<PartDesc*>(p.desc)[blockIdx.x] = e;
+      }
+      if (!w.has(t)) {  // none of this tile's blocks are in this piece
+        if (real && !whole) {
+          p.part_ml[2 * part] = -INFINITY;
+          p.part_ml[2 * part + 1] = 0.0f;
+        }
+        continue;
+      }
+      float c_log2 = p.scale_log2, v_mult = 1.0f;
+      if constexpr (FP8) {
+        // this row of Q as fp16, its largest element brought to [1/2, 1)
+        constexpr int W = DQK / 2;
+        uint32_t q[W];
+        const uint4* src = reinterpret_cast<const uint4*>(
+            p.q + (w.r.t0 + (real ? tok : 0)) * p.q_stride + static_cast<int64_t>(w.h * p.G + (real ? rhead : 0)) * DQK);
+        float amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i) {
+          const uint4 x = real ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+          q[4 * i] = x.x, q[4 * i + 1] = x.y, q[4 * i + 2] = x.z, q[4 * i + 3] = x.w;
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(q[i] << 16)), fabsf(__uint_as_float(q[i] & 0xffff0000u))));
+        int e = 0;
+        if (amax > 0.0f && amax < INFINITY) e = max(-126, min(126, static_cast<int>(__float_as_uint(amax) >> 23) - 126));
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        c_log2 *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * __ldg(p.k_scale + w.h);
+        v_mult = __ldg(p.v_scale + w.h);
+        if (units > 0) ok = paged_wait(bQEmpty + 8 * t, (units - 1) & 1, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i) {
+          uint32_t y[4];
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+            y[n] = pack_f16x2(__uint_as_float(q[4 * i + n] << 16) * down, __uint_as_float(q[4 * i + n] & 0xffff0000u) * down);
+          st_shared_v4(sQ + t * C::Q_BYTES + (i >> 3) * C::CHUNK + r * 128 + (((i & 7) ^ (r & 7)) << 4), y[0], y[1], y[2],
+                       y[3]);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bQFull + 8 * t);
+      }
+      ++units;
+      c_log2 = fmaxf(c_log2, 1e-30f);  // a zero scale behaves as a tiny one
+      // keys this row sees: j <= see; the tile's first row sees fewest
+      const int off = p.causal ? w.r.kv - w.r.nq : w.r.kv - 1;
+      const int see = p.causal ? min(off + tok, w.r.kv - 1) : off;
+      const int see_all = p.causal ? min(off + (2 * w.pair + t) * tpt, w.r.kv - 1) : off;
+
+      float m_run = -INFINITY, l_run = 0.0f;
+      const int end = w.end(t);
+      for (int j = w.kb; j < end; ++j, ++g) {
+        ok = __all_sync(0xffffffffu, paged_wait(bSFull + 8 * t, g & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sr[128];
+        tmem_ld32(tS + 0, sr);
+        tmem_ld32(tS + 32, sr + 32);
+        tmem_ld32(tS + 64, sr + 64);
+        tmem_ld32(tS + 96, sr + 96);
+        tmem_ld_wait32(sr);
+        reg_fence32(sr + 32);
+        reg_fence32(sr + 64);
+        reg_fence32(sr + 96);
+        tc_fence_before();
+        mbar_arrive(bSFree);  // S may take the next product now
+
+        const int kv0 = j * kChN;
+        if (kv0 + kChN - 1 > see_all) {
+          const int lim = see - kv0;
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c > lim) sr[c] = __float_as_uint(-INFINITY);
+        }
+        // row maximum; a NaN score stays one
+        float x0 = __uint_as_float(sr[0]), x1 = __uint_as_float(sr[1]);
+        float x2 = __uint_as_float(sr[2]), x3 = __uint_as_float(sr[3]);
+#pragma unroll
+        for (int c = 4; c < 124; c += 8) {
+          x0 = max3_nan(x0, __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+          x1 = max3_nan(x1, __uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]));
+          x2 = max3_nan(x2, __uint_as_float(sr[c + 4]), __uint_as_float(sr[c + 5]));
+          x3 = max3_nan(x3, __uint_as_float(sr[c + 6]), __uint_as_float(sr[c + 7]));
+        }
+        x0 = max3_nan(x0, __uint_as_float(sr[124]), __uint_as_float(sr[125]));
+        x1 = max3_nan(x1, __uint_as_float(sr[126]), __uint_as_float(sr[127]));
+        x0 = max3_nan(x0, x1, x2);
+        const float m_new = max3_nan(m_run, x0 * c_log2, x3 * c_log2);
+        const bool need = !(m_new <= m_run + C::T_LAG);  // true for NaN too
+        float alpha = 1.0f;
+        if (need) {
+          alpha = ex2_approx(m_run - m_new);
+          m_run = m_new;
+        }
+        l_run *= alpha;
+
+        // probabilities, packed in place; a row that has seen nothing yet has m = -inf and only masked scores
+        const float nm = m_run == -INFINITY ? 0.0f : -m_run;
+        float sa = 0.f, sb = 0.f, sc = 0.f, sd = 0.f;
+#pragma unroll
+        for (int c = 0; c < 128; c += 4) {
+          float y0, y1, y2, y3, p0, p1, p2, p3;
+          ffma2_bcast(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]), c_log2, nm, y0, y1);
+          ffma2_bcast(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]), c_log2, nm, y2, y3);
+          if ((c & 12) == 12) {  // one score in four off the MUFU unit
+            ch_exp2_fma(y0, y1, p0, p1);
+            ch_exp2_fma(y2, y3, p2, p3);
+          } else {
+            p0 = ex2_approx(y0);
+            p1 = ex2_approx(y1);
+            p2 = ex2_approx(y2);
+            p3 = ex2_approx(y3);
+          }
+          fadd2(sa, sb, p0, p1);
+          fadd2(sc, sd, p2, p3);
+          sr[c >> 1] = FP8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+          sr[(c >> 1) + 1] = FP8 ? pack_f16x2(p2, p3) : pack_bf16x2(p2, p3);
+        }
+        l_run += (sa + sb) + (sc + sd);
+
+        // P and O are free once PV of the tile's block before has completed
+        bool w_ok = g == 0 || paged_wait(bPDone + 8 * t, (g - 1) & 1, abort_flag);
+        const bool resc = j > w.kb && __any_sync(0xffffffffu, need);
+        ok = __all_sync(0xffffffffu, w_ok);
+        if (!ok) break;
+        tc_fence_after();
+        if (resc) {
+#pragma unroll 1
+          for (int cc = 0; cc < DV; cc += 32) {
+            uint32_t orr[32];
+            tmem_ld32(tO + cc, orr);
+            tmem_ld_wait32(orr);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) orr[i] = __float_as_uint(__uint_as_float(orr[i]) * alpha);
+            tmem_st32(tO + cc, orr);
+          }
+        }
+        tmem_st32(tP, sr);
+        tmem_st32(tP + 32, sr + 32);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bPFull + 8 * t);
+      }
+      if (!ok) break;
+
+      ok = __all_sync(0xffffffffu, paged_wait(bOFull + 8 * t, (units - 1) & 1, abort_flag));
+      if (!ok) break;
+      tc_fence_after();
+      const float inv = !whole ? 1.0f : (l_run == 0.0f ? 0.0f : v_mult / l_run);
+      const int hq = w.h * p.G + rhead;
+      __nv_bfloat16* orow = p.o + (static_cast<int64_t>(w.r.t0 + (real ? tok : 0)) * p.Hq + (real ? hq : 0)) * DV;
+      float* prow = p.part_o + (real ? part : 0) * DV;
+#pragma unroll 1
+      for (int cc = 0; cc < DV; cc += 32) {
+        uint32_t orr[32];
+        tmem_ld32(tO + cc, orr);
+        tmem_ld_wait32(orr);
+        if (real && whole) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint4 y;
+            y.x = pack_bf16x2(__uint_as_float(orr[8 * i]) * inv, __uint_as_float(orr[8 * i + 1]) * inv);
+            y.y = pack_bf16x2(__uint_as_float(orr[8 * i + 2]) * inv, __uint_as_float(orr[8 * i + 3]) * inv);
+            y.z = pack_bf16x2(__uint_as_float(orr[8 * i + 4]) * inv, __uint_as_float(orr[8 * i + 5]) * inv);
+            y.w = pack_bf16x2(__uint_as_float(orr[8 * i + 6]) * inv, __uint_as_float(orr[8 * i + 7]) * inv);
+            *reinterpret_cast<uint4*>(orow + cc + 8 * i) = y;
+          }
+        } else if (real) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4*>(prow + cc + 4 * i) =
+                make_uint4(orr[4 * i], orr[4 * i + 1], orr[4 * i + 2], orr[4 * i + 3]);
+        }
+      }
+      if (real && !whole) {
+        p.part_ml[2 * part] = m_run;
+        p.part_ml[2 * part + 1] = l_run;
+      } else if (real && p.lse != nullptr) {
+        p.lse[static_cast<int64_t>(hq) * p.T + w.r.t0 + tok] =
+            l_run == 0.0f ? -INFINITY : (m_run + fast_log2(l_run)) * kLn2;
+      }
+      tc_fence_before();
+      mbar_arrive(bOEmpty + 8 * t);
+    }
+  } else {
+    // ------------------------------------------------------------ e4m3 -> fp16 tiles
+    if constexpr (FP8) {
+      setmaxnreg_dec<C::REGS_CONV>();
+      const int tid = threadIdx.x - 384;
+      ChRegs<DQK> kr;
+      ChRegs<DV> vr;
+      uint32_t it = 0;
+      bool ok = true;
+      // lane i holds the page of 16-key group i of the block to load
+      ChWalk nx(p, d, tpt);  // runs one block ahead
+      int nj = nx.kb;
+      auto pages_of = [&]() { return lane < 8 ? paged_page(p, nx.b, nj * kChN + 16 * lane, nx.r.kv) : 0; };
+      int pages = 0;
+      bool more = nx.valid();
+      if (more) {
+        pages = pages_of();
+        kr.load(codes, 0, nx.h, nj * kChN, nx.r.kv, pages, p.page_size, p.num_pages, tid);
+        vr.load(codes, 1, nx.h, nj * kChN, nx.r.kv, pages, p.page_size, p.num_pages, tid);
+      }
+      for (; more && ok; ++it) {
+        const uint32_t ks = it % C::SK, vs = it % C::SV;
+        if (++nj >= nx.ke) {
+          nx.next();
+          nj = nx.kb;
+          more = nx.valid();
+        }
+        if (more) pages = pages_of();
+        if (it >= C::SK) ok = __all_sync(0xffffffffu, paged_wait(bKEmpty + 8 * ks, ((it / C::SK) - 1) & 1, abort_flag));
+        if (!ok) break;
+        kr.store(sK + ks * C::K_BYTES, tid);
+        fence_proxy_async_smem();
+        mbar_arrive(bKFull + 8 * ks);
+        if (more) kr.load(codes, 0, nx.h, nj * kChN, nx.r.kv, pages, p.page_size, p.num_pages, tid);
+        if (it >= C::SV) ok = __all_sync(0xffffffffu, paged_wait(bVEmpty + 8 * vs, ((it / C::SV) - 1) & 1, abort_flag));
+        if (!ok) break;
+        vr.store(sV + vs * C::V_BYTES, tid);
+        fence_proxy_async_smem();
+        mbar_arrive(bVFull + 8 * vs);
+        if (more) vr.load(codes, 1, nx.h, nj * kChN, nx.r.kv, pages, p.page_size, p.num_pages, tid);
+      }
+    }
+  }
+
+  // -------------------------------------------------------------- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace b200p

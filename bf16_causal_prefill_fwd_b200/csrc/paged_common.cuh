@@ -26,7 +26,7 @@ __device__ __forceinline__ void paged_report(int code) { atomicCAS(&g_paged_stat
 
 // Bounded mbarrier wait, as the prefill kernels have it: false if it gave up
 // after two seconds or another role of the block already had.
-__device__ __noinline__ bool paged_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+__device__ __forceinline__ bool paged_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   const uint64_t t0 = global_timer_ns();
   while (true) {
     if (mbar_try_wait_suspend(bar, parity, 1000000u)) return true;
@@ -126,6 +126,7 @@ struct PagedAttn {
   int* desc;         // workspace: one PartDesc per block
   float* part_ml;    // workspace: (m, l) per slot and row
   float* part_o;     // workspace: O per slot and row
+  int slot_rows;     // rows of a slot
 };
 
 // One request as the kernels see it; tiles == 0: nothing is computed for it.

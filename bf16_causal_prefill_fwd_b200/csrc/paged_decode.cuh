@@ -499,8 +499,8 @@ __global__ void __launch_bounds__(kDecThreads, kDecBlocksPerSm)
               p.lse[static_cast<int64_t>(hq) * p.T + w.r.t0 + tok] =
                   ll == 0.0f ? -INFINITY : (mm + fast_log2(ll)) * kLn2;
           } else {
-            p.part_o[(static_cast<int64_t>(slot) * kDecMaxRows + r) * DV + td] = acc;
-            if (td < 2) p.part_ml[(slot * kDecMaxRows + r) * 2 + td] = td == 0 ? mm : ll;
+            p.part_o[(static_cast<int64_t>(slot) * p.slot_rows + r) * DV + td] = acc;
+            if (td < 2) p.part_ml[(slot * p.slot_rows + r) * 2 + td] = td == 0 ? mm : ll;
           }
         }
       }
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecBlocksPerSm)
 // Joins the parts of the units that several blocks have worked on: block c
 // takes the unit that begins, but does not end, in block c. Parts are added in
 // block order. Rows are spread over gridDim.y.
-template <int DV, int MAX_ROWS>
+template <int DV>
 __global__ void __launch_bounds__(DV) paged_join_kernel(const PagedAttn p) {
   pdl_wait();
   const int c = blockIdx.x, td = threadIdx.x;
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(DV) paged_join_kernel(const PagedAttn p) {
   for (int r = blockIdx.y; r < e.nrows; r += gridDim.y) {
     float mm = -INFINITY, ll = 0.0f, acc = 0.0f;
     for (int b = c; b <= e.last; ++b) {
-      const int64_t at = static_cast<int64_t>(2 * b + (b == c ? 1 : 0)) * MAX_ROWS + r;
+      const int64_t at = static_cast<int64_t>(2 * b + (b == c ? 1 : 0)) * p.slot_rows + r;
       const float m = p.part_ml[2 * at], l = p.part_ml[2 * at + 1];
       if (l == 0.0f) continue;  // this part saw none of the row's keys
       const float mn = fmaxf(mm, m);

@@ -74,6 +74,62 @@ def test_decode_softmax_scale_and_large_scores():
     check_attention(p, o, lse, softmax_scale=0.3)
 
 
+# ------------------------------------------------------------------------------------------- many rows (chunks)
+
+CHUNK_LENS = [
+    ([17], [17]),                                        # a prompt's first chunk
+    ([33, 1, 0, 64, 5], [33, 700, 40, 64, 1300]),        # chunks and decoding requests together
+    ([200, 130], [1000, 130]),
+    ([65, 40, 20], [30, 0, 257]),                        # more new tokens than keys: rows that see nothing
+]
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("heads", SHAPES)
+@pytest.mark.parametrize("lens", CHUNK_LENS)
+def test_chunk_matches_the_plain_form(lens, heads, e4m3):
+    p = make(*lens, *heads, page_size=16, e4m3=e4m3, seed=sum(lens[0]))
+    o, lse = run(p)
+    check_attention(p, o, lse)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("page_size", [16, 48, 64, 96, 128, 256])
+def test_chunk_page_sizes(page_size, e4m3):
+    p = make([70, 9], [3 * page_size + 70, page_size + 1], 8, 2, 128, page_size, e4m3, seed=page_size)
+    o, lse = run(p, max_seqlen_q=70)
+    check_attention(p, o, lse)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_chunk_without_the_causal_mask(e4m3):
+    p = make([50, 150, 3], [400, 1, 129], 8, 2, 128, 32, e4m3, seed=5)
+    o, lse = run(p, causal=False)
+    check_attention(p, o, lse, causal=False)
+
+
+@pytest.mark.parametrize("heads", [(128, 1, 128), (5, 1, 128), (48, 2, 192)])
+def test_large_and_odd_groups(heads):
+    """A group of 128 heads is one token per tile; five heads leave rows of a tile unused."""
+    p = make([7, 30], [300, 90], *heads, page_size=16, seed=heads[0])
+    o, lse = run(p)
+    check_attention(p, o, lse)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_chunk_of_one_long_request_is_split_over_the_gpu(e4m3):
+    p = make([40], [9000], 4, 1, 128, 64, e4m3, seed=17)
+    o, lse = run(p)
+    check_attention(p, o, lse)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_chunk_large_scores(e4m3):
+    p = make([130], [700], 4, 2, 128, 16, e4m3, seed=18, spread=6.0)
+    o, lse = run(p, softmax_scale=0.3)
+    check_attention(p, o, lse, softmax_scale=0.3)
+
+
 # ------------------------------------------------------------------------------------------- slots
 
 def plain_slots(table, ctx, new, total, ps, free=None, head=0):
