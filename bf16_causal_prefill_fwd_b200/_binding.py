@@ -27,16 +27,6 @@ BLOCK = 128
 _lib = None
 
 
-class PagedCache(ctypes.Structure):
-    """b200attn_paged_cache of the header."""
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
-                ("k_page_stride", ctypes.c_int64), ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
-                ("v_page_stride", ctypes.c_int64), ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
-                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("Hkv", ctypes.c_int),
-                ("d_qk", ctypes.c_int), ("d_v", ctypes.c_int), ("dtype", ctypes.c_int),
-                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
-
-
 class B200AttnError(RuntimeError):
     def __init__(self, code: int, what: str):
         msg = _lib.b200attn_strerror(code).decode() if _lib is not None else "library not loaded"

@@ -14,104 +14,115 @@ graph and replayed on new contents.
 from __future__ import annotations
 
 import contextlib
-import ctypes
+import struct
 
 import torch
 
 from . import _binding as _b
 
-_MAX_GROUP = 128
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+# b200attn_paged_cache of the header
+_CACHE = struct.Struct("@2P6q6i2P")
 
 
-def _check_cuda(name, t, dtype, dim):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype or t.dim() != dim:
-        raise ValueError(f"{name} must be a {dim}-D {dtype} tensor")
+def _is_cuda(t):
+    return isinstance(t, torch.Tensor) and t.is_cuda
 
 
 def _check_ints(name, t, shape, device):
-    _check_cuda(name, t, torch.int32, len(shape))
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not (_is_cuda(t) and t.dtype is _I32 and t.shape == shape and t.device == device and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on {device}")
 
 
 def _check_table(t, batch, device):
-    _check_cuda("block_table", t, torch.int32, 2)
-    if t.device != device:
-        raise ValueError(f"block_table must be on {device}")
-    if t.shape[0] != batch or t.shape[1] < 1:
+    """The row stride of a block table."""
+    if not (_is_cuda(t) and t.dtype is _I32 and t.dim() == 2 and t.device == device):
+        raise ValueError(f"block_table must be a 2-D int32 tensor on {device}")
+    (rows, width), (row, col) = t.shape, t.stride()
+    if rows != batch or width < 1:
         raise ValueError(f"block_table must have shape [{batch}, pages], got {tuple(t.shape)}")
-    if (t.shape[1] > 1 and t.stride(1) != 1) or (batch > 1 and t.stride(0) < t.shape[1]):
+    if rows == 1:
+        row = width
+    if (width > 1 and col != 1) or row < width:
         raise ValueError("block_table must have contiguous rows that do not overlap")
+    return row
 
 
 def _check_rows(name, t, heads, d, device):
     """bf16 [tokens, heads, d], each token contiguous, tokens any multiple of 8
-    elements apart (a slice of a fused projection's output)."""
-    _check_cuda(name, t, torch.bfloat16, 3)
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    if (heads is not None and t.shape[1] != heads) or t.shape[2] != d:
+    elements apart (a slice of a fused projection's output): their distance."""
+    if not (_is_cuda(t) and t.dtype is _BF16 and t.dim() == 3 and t.device == device):
+        raise ValueError(f"{name} must be a 3-D bf16 tensor on {device}")
+    (_, h, dim), (token, head, one) = t.shape, t.stride()
+    if (heads is not None and h != heads) or h < 1 or dim != d:
         raise ValueError(f"{name} must have shape [tokens, {heads or 'heads'}, {d}], got {tuple(t.shape)}")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d) or t.stride(0) % 8 != 0:
+    if one != 1 or (h > 1 and head != d) or token % 8 != 0:
         raise ValueError(f"{name} must have contiguous heads and a token stride that is a multiple of 8 elements")
+    return token
 
 
-def _strides(name, c):
+def _strides(name, c, esz):
     """(page, token, head) strides in elements; those of dimensions of one are replaced by what they would be."""
-    esz = c.element_size()
-    P, ps, H, d = c.shape
-    if c.stride(3) != 1:
+    (P, ps, H, d), (page, token, head, one) = c.shape, c.stride()
+    if P == 1:
+        page = ps * H * d
+    if ps == 1:
+        token = H * d
+    if H == 1:
+        head = d
+    if one != 1:
         raise ValueError(f"{name} must have contiguous rows (d fastest)")
-    out = []
-    for size, stride, usual in ((P, c.stride(0), ps * H * d), (ps, c.stride(1), H * d), (H, c.stride(2), d)):
-        if size == 1:
-            stride = usual
-        if stride <= 0 or stride * esz % 16 != 0:
-            raise ValueError(f"{name}'s strides must be positive multiples of 16 bytes")
-        out.append(stride)
-    return out
+    if page <= 0 or token <= 0 or head <= 0 or (page | token | head) * esz & 15:
+        raise ValueError(f"{name}'s strides must be positive multiples of 16 bytes")
+    return page, token, head
 
 
 def _cache(k_cache, v_cache, k_scale, v_scale):
-    """Checks the cache tensors and describes them to the library."""
-    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if not isinstance(c, torch.Tensor) or not c.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if c.dim() != 4:
-            raise ValueError(f"{name} must be 4-D [pages, page_size, H, d]")
-    if k_cache.device != v_cache.device:
+    """Checks the cache tensors: (description for the library, Hkv, d_qk, d_v)."""
+    if not (_is_cuda(k_cache) and _is_cuda(v_cache)):
+        raise ValueError("k_cache and v_cache must be CUDA tensors")
+    if k_cache.dim() != 4 or v_cache.dim() != 4:
+        raise ValueError("k_cache and v_cache must be 4-D [pages, page_size, H, d]")
+    dev, dtype = k_cache.device, k_cache.dtype
+    (P, ps, H, d_qk), d_v = k_cache.shape, v_cache.shape[3]
+    if v_cache.device != dev:
         raise ValueError("k_cache and v_cache must be on one device")
-    if k_cache.shape[:3] != v_cache.shape[:3] or k_cache.dtype != v_cache.dtype:
+    if v_cache.shape != (P, ps, H, d_v) or v_cache.dtype is not dtype:
         raise ValueError("k_cache and v_cache must agree in pages, page_size, heads and dtype")
-    fp8 = _b._is_fp8(k_cache)
-    if not fp8 and k_cache.dtype != torch.bfloat16:
-        raise ValueError("the cache must be bf16 or e4m3")
-    P, ps, H, d_qk = k_cache.shape
-    if min(P, ps, H) < 1:
+    if P < 1 or ps < 1 or H < 1:
         raise ValueError("the cache must hold at least one page, row and head")
-    if fp8:
+    if dtype is _BF16:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("scales are for e4m3 caches")
+        esz, code, ks, vs = 2, _b.BF16, 0, 0
+    elif _b._is_fp8(k_cache):
         for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
             if s is None:
                 raise ValueError(f"{name} is required for an e4m3 cache")
-            _check_cuda(name, s, torch.float32, 1)
-            if s.device != k_cache.device or s.shape[0] != H or not s.is_contiguous():
-                raise ValueError(f"{name} must be contiguous fp32 [{H}] on {k_cache.device}")
-    elif k_scale is not None or v_scale is not None:
-        raise ValueError("scales are for e4m3 caches")
-    return _b.PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), *_strides("k_cache", k_cache),
-                         *_strides("v_cache", v_cache), P, ps, H, d_qk, v_cache.shape[3], _b.FP8_E4M3 if fp8 else _b.BF16,
-                         _b._ptr(k_scale) if fp8 else None, _b._ptr(v_scale) if fp8 else None)
+            if not (_is_cuda(s) and s.dtype is _F32 and s.shape == (H,) and s.device == dev and s.is_contiguous()):
+                raise ValueError(f"{name} must be contiguous fp32 [{H}] on {dev}")
+        esz, code, ks, vs = 1, _b.FP8_E4M3, k_scale.data_ptr(), v_scale.data_ptr()
+    else:
+        raise ValueError("the cache must be bf16 or e4m3")
+    return _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), *_strides("k_cache", k_cache, esz),
+                       *_strides("v_cache", v_cache, esz), P, ps, H, d_qk, d_v, code, ks, vs), H, d_qk, d_v
+
+
+_HERE = contextlib.nullcontext()
 
 
 def _on(device):
     """The tensors' device as the current one."""
-    if device.type != "cuda" or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+    if device.type != "cuda" or device.index == torch._C._cuda_getDevice():
+        return _HERE
     return torch.cuda.device(device)
+
+
+def _stream(stream, device):
+    """The stream to launch on: the current one of the tensors' device by default."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return _b._stream_handle(stream)
 
 
 def _done(rc, what):
@@ -131,40 +142,40 @@ def paged_slots(block_table, context_lens, new_lens, total: int, page_size: int,
     fit, -6 for too few free pages.
     """
     lib = _b.load_library()
-    if not isinstance(context_lens, torch.Tensor) or context_lens.dim() != 1 or context_lens.shape[0] < 1:
+    if not _is_cuda(context_lens) or context_lens.dim() != 1 or context_lens.shape[0] < 1:
         raise ValueError("context_lens must be an int32 [batch] CUDA tensor")
     B, dev = context_lens.shape[0], context_lens.device
     _check_ints("context_lens", context_lens, (B,), dev)
     _check_ints("new_lens", new_lens, (B,), dev)
-    _check_table(block_table, B, dev)
+    row = _check_table(block_table, B, dev)
     total, page_size = int(total), int(page_size)
     if total < 0 or page_size < 1:
         raise ValueError("total must not be negative and page_size at least 1")
-    if free_pages is None:
-        if free_head is not None or free_head_out is not None:
-            raise ValueError("free_head goes with free_pages")
-    else:
-        if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
+    free, count, head, head_out = None, 0, None, None
+    if free_pages is not None:
+        if not _is_cuda(free_pages) or free_pages.dim() != 1:
             raise ValueError("free_pages must be an int32 [pages] CUDA tensor")
-        _check_ints("free_pages", free_pages, (free_pages.shape[0],), dev)
+        count = free_pages.shape[0]
+        _check_ints("free_pages", free_pages, (count,), dev)
         _check_ints("free_head", free_head, (1,), dev)
-        if free_head_out is None:
-            free_head_out = torch.empty(1, dtype=torch.int32, device=dev)
-        else:
+        if free_head_out is not None:
             _check_ints("free_head_out", free_head_out, (1,), dev)
-    out = torch.empty(2 * B + 1 + 2 * total, dtype=torch.int32, device=dev)
-    cu, kv, pos, slots = out.split((B + 1, B, total, total))
-    if free_pages is not None and free_pages.shape[0] == 0:
-        free_pages = torch.zeros(1, dtype=torch.int32, device=dev)  # an address; none of it is free
-        count = 0
-    else:
-        count = 0 if free_pages is None else free_pages.shape[0]
+        head = free_head.data_ptr()
+        free = free_pages.data_ptr() or head  # an empty list needs an address; none of it is read
+    elif free_head is not None or free_head_out is not None:
+        raise ValueError("free_head goes with free_pages")
+    out = torch.empty(2 * B + 2 + 2 * total, dtype=_I32, device=dev)
+    cu, kv, pos, slots, new_head = out.split_with_sizes((B + 1, B, total, total, 1))
+    at = out.data_ptr()
+    if free_pages is not None:
+        if free_head_out is None:
+            free_head_out = new_head
+        head_out = free_head_out.data_ptr()
     with _on(dev):
         _done(lib.b200attn_paged_slots(
-            _b._ptr(block_table), block_table.stride(0) if B > 1 else block_table.shape[1], block_table.shape[1],
-            _b._ptr(context_lens), _b._ptr(new_lens), B, total, page_size, _b._ptr(free_pages), count,
-            _b._ptr(free_head), _b._ptr(free_head_out), _b._ptr(cu), _b._ptr(kv), _b._ptr(pos), _b._ptr(slots),
-            _b._stream_handle(stream)), "b200attn_paged_slots")
+            block_table.data_ptr(), row, block_table.shape[1], context_lens.data_ptr(), new_lens.data_ptr(), B, total,
+            page_size, free, count, head, head_out, at, at + 4 * (B + 1), at + 4 * (2 * B + 1),
+            at + 4 * (2 * B + 1 + total), _stream(stream, dev)), "b200attn_paged_slots")
     return (cu, kv, pos, slots) if free_pages is None else (cu, kv, pos, slots, free_head_out)
 
 
@@ -173,16 +184,17 @@ def paged_append_kv(k, v, k_cache, v_cache, slots, *, k_scale=None, v_scale=None
     are taken as they are) to the cache rows ``slots`` (int32 [total]; negative: the row is skipped), as bf16 or as
     e4m3(x / scale) with one fp32 scale per head, via b200attn_paged_append. Returns (k_cache, v_cache)."""
     lib = _b.load_library()
-    c = _cache(k_cache, v_cache, k_scale, v_scale)
+    cache, H, d_qk, d_v = _cache(k_cache, v_cache, k_scale, v_scale)
     dev = k_cache.device
-    _check_rows("k", k, c.Hkv, c.d_qk, dev)
-    _check_rows("v", v, c.Hkv, c.d_v, dev)
-    if k.shape[0] != v.shape[0]:
+    k_row = _check_rows("k", k, H, d_qk, dev)
+    v_row = _check_rows("v", v, H, d_v, dev)
+    total = k.shape[0]
+    if v.shape[0] != total:
         raise ValueError("k and v must have the same number of tokens")
-    _check_ints("slots", slots, (k.shape[0],), dev)
+    _check_ints("slots", slots, (total,), dev)
     with _on(dev):
-        _done(lib.b200attn_paged_append(_b._ptr(k), _b._ptr(v), k.stride(0), v.stride(0), k.shape[0], ctypes.addressof(c),
-                                        _b._ptr(slots), _b._stream_handle(stream)), "b200attn_paged_append")
+        _done(lib.b200attn_paged_append(k.data_ptr(), v.data_ptr(), k_row, v_row, total, cache, slots.data_ptr(),
+                                        _stream(stream, dev)), "b200attn_paged_append")
     return k_cache, v_cache
 
 
@@ -202,41 +214,42 @@ def attn_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, *, max
     [Hq, total]); rows of no request are left unwritten.
     """
     lib = _b.load_library()
-    c = _cache(k_cache, v_cache, k_scale, v_scale)
+    cache, Hkv, d_qk, d_v = _cache(k_cache, v_cache, k_scale, v_scale)
     dev = k_cache.device
-    _check_rows("q", q, None, c.d_qk, dev)
+    q_row = _check_rows("q", q, None, d_qk, dev)
     total, Hq, _ = q.shape
-    if Hq % c.Hkv != 0:
+    if Hq % Hkv != 0:
         raise ValueError("the query heads must be a multiple of the cache's heads")
-    if not isinstance(kv_lens, torch.Tensor) or kv_lens.dim() != 1 or kv_lens.shape[0] < 1:
+    if not _is_cuda(kv_lens) or kv_lens.dim() != 1 or kv_lens.shape[0] < 1:
         raise ValueError("kv_lens must be an int32 [batch] CUDA tensor")
     B = kv_lens.shape[0]
     _check_ints("kv_lens", kv_lens, (B,), dev)
     _check_ints("cu_seqlens", cu_seqlens, (B + 1,), dev)
-    _check_table(block_table, B, dev)
+    row = _check_table(block_table, B, dev)
     max_q = total if max_seqlen_q is None else int(max_seqlen_q)
     if max_q < 1 and total > 0:
         raise ValueError("max_seqlen_q must be at least 1")
     if out is None:
-        out = torch.empty((total, Hq, c.d_v), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((total, Hq, d_v), dtype=_BF16, device=dev)
     else:
-        _b._check_buffer("out", out, (total, Hq, c.d_v), (torch.bfloat16,), dev)
-    lse = torch.empty((Hq, total), dtype=torch.float32, device=dev) if return_lse else None
+        _b._check_buffer("out", out, (total, Hq, d_v), (_BF16,), dev)
+    lse = torch.empty((Hq, total), dtype=_F32, device=dev) if return_lse else None
     if total == 0:
         return (out, lse) if return_lse else out
     max_q = min(max_q, total)
     if workspace is None:
-        workspace = torch.empty(max(16, attn_paged_workspace_bytes(total, max_q, Hq, c.Hkv)), dtype=torch.uint8,
-                                device=dev)
-    elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous on {dev}")
+        size = lib.b200attn_paged_fwd_workspace_bytes(total, max_q, Hq, Hkv)
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+    else:
+        if not _is_cuda(workspace) or workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on {dev}")
+        size = workspace.numel() * workspace.element_size()
     with _on(dev):
         _done(lib.b200attn_paged_fwd(
-            _b._ptr(q), q.stride(0), ctypes.addressof(c), _b._ptr(block_table),
-            block_table.stride(0) if B > 1 else block_table.shape[1], block_table.shape[1], _b._ptr(cu_seqlens),
-            _b._ptr(kv_lens), B, total, max_q, Hq, 1 if causal else 0, float(softmax_scale) if softmax_scale else 0.0,
-            _b._ptr(out), _b._ptr(lse), _b._ptr(workspace), workspace.numel() * workspace.element_size(),
-            _b._stream_handle(stream)), "b200attn_paged_fwd")
+            q.data_ptr(), q_row, cache, block_table.data_ptr(), row, block_table.shape[1], cu_seqlens.data_ptr(),
+            kv_lens.data_ptr(), B, total, max_q, Hq, 1 if causal else 0, float(softmax_scale) if softmax_scale else 0.0,
+            out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(), size, _stream(stream, dev)),
+              "b200attn_paged_fwd")
     return (out, lse) if return_lse else out
 
 

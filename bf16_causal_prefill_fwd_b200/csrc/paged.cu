@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -48,15 +49,44 @@ int gcd(int a, int b) {
   return a;
 }
 
-// Compute capability 10.0; *sm_count: SMs of the current device.
-int device_ok(int* sm_count) {
-  int dev = 0, major = 0, minor = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(sm_count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+constexpr int kDevices = 64;
+
+// Compute capability 10.0; *sm_count: SMs of the current device (looked up once
+// per device), *device: its number.
+int device_ok(int* sm_count, int* device) {
+  static std::atomic<int> sms[kDevices];  // 0: not looked up yet, -1: not supported
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return B200ATTN_ERR_CUDA;
+  int n = sms[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return B200ATTN_ERR_CUDA;
+    if (major != 10 || minor != 0) n = -1;
+    sms[dev].store(n, std::memory_order_relaxed);
+  }
+  if (n < 0) return B200ATTN_ERR_UNSUPPORTED;
+  *sm_count = n;
+  *device = dev;
+  return B200ATTN_OK;
+}
+
+// Lets `kern` use `bytes` of dynamic shared memory, once per kernel and device
+// (`done` is the kernel's own). With `regs`, the kernel must have been built with
+// that many registers per thread: a role split (setmaxnreg) of another launch
+// allocation would wait for registers that do not exist.
+int prepare_kernel(const void* kern, int bytes, int regs, int device, std::atomic<uint64_t>& done) {
+  const uint64_t bit = uint64_t(1) << device;
+  if (done.load(std::memory_order_acquire) & bit) return B200ATTN_OK;
+  cudaFuncAttributes a;
+  if (cudaFuncGetAttributes(&a, kern) != cudaSuccess ||
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return B200ATTN_ERR_CUDA;
-  return major == 10 && minor == 0 ? B200ATTN_OK : B200ATTN_ERR_UNSUPPORTED;
+  if (regs != 0 && a.numRegs != regs) return B200ATTN_ERR_UNSUPPORTED;
+  done.fetch_or(bit, std::memory_order_release);
+  return B200ATTN_OK;
 }
 
 // A stride the kernels may use: a multiple of 16 bytes, not negative.
@@ -144,16 +174,17 @@ Parts parts_of(int blocks, int rows) {
 bool few_rows(int max_q, int G) { return static_cast<int64_t>(max_q) * G <= b200p::kDecMaxRows; }
 
 template <int DQK, bool FP8, int NT>
-int launch_decode(const b200attn_paged_cache* c, PagedAttn p, int sm_count, cudaStream_t st) {
+int launch_decode(const b200attn_paged_cache* c, PagedAttn p, int sm_count, int device, cudaStream_t st) {
   using C = b200p::DecCfg<DQK, 128, FP8, NT>;
   p.box = gcd(p.page_size, b200p::kDecKeys);
   p.slot_rows = b200p::kDecMaxRows;
   CUtensorMap tk, tv;
   if (!page_maps(&tk, &tv, c, p.box)) return B200ATTN_ERR_CUDA;
   auto kern = b200p::paged_decode_kernel<DQK, 128, FP8, NT>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
-    return B200ATTN_ERR_CUDA;
-  int blocks = b200p::kDecBlocksPerSm * sm_count;
+  static std::atomic<uint64_t> done{0};
+  const int rc = prepare_kernel(reinterpret_cast<const void*>(kern), C::SMEM, 0, device, done);
+  if (rc != B200ATTN_OK) return rc;
+  int blocks = C::BLOCKS * sm_count;
   if (blocks > b200p::kDecMaxBlocks) blocks = b200p::kDecMaxBlocks;
   kern<<<blocks, b200p::kDecThreads, C::SMEM, st>>>(tk, tv, p);
   if (cudaGetLastError() != cudaSuccess) return B200ATTN_ERR_CUDA;
@@ -162,9 +193,9 @@ int launch_decode(const b200attn_paged_cache* c, PagedAttn p, int sm_count, cuda
 }
 
 template <int DQK, bool FP8>
-int launch_few(const b200attn_paged_cache* c, const PagedAttn& p, int sm_count, cudaStream_t st) {
-  if (p.max_q * p.G <= 8) return launch_decode<DQK, FP8, 1>(c, p, sm_count, st);
-  return launch_decode<DQK, FP8, 2>(c, p, sm_count, st);
+int launch_few(const b200attn_paged_cache* c, const PagedAttn& p, int sm_count, int device, cudaStream_t st) {
+  if (p.max_q * p.G <= 8) return launch_decode<DQK, FP8, 1>(c, p, sm_count, device, st);
+  return launch_decode<DQK, FP8, 2>(c, p, sm_count, device, st);
 }
 
 // Rows of a workspace slot of the many-rows kernel.
@@ -174,7 +205,7 @@ int chunk_rows(int total, int G) {
 }
 
 template <int DQK, bool FP8>
-int launch_chunk(const b200attn_paged_cache* c, PagedAttn p, int sm_count, cudaStream_t st) {
+int launch_chunk(const b200attn_paged_cache* c, PagedAttn p, int sm_count, int device, cudaStream_t st) {
   using C = b200p::ChCfg<DQK, 128, FP8>;
   p.box = gcd(p.page_size, b200p::kChN);
   p.slot_rows = chunk_rows(p.T, p.G);
@@ -199,15 +230,9 @@ int launch_chunk(const b200attn_paged_cache* c, PagedAttn p, int sm_count, cudaS
     if (!page_maps(&tk, &tv, c, p.box)) return B200ATTN_ERR_CUDA;
   }
   auto kern = b200p::paged_chunk_kernel<DQK, 128, FP8>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
-    return B200ATTN_ERR_CUDA;
-  // The role split (setmaxnreg) hands out registers from the block's launch
-  // allocation: a build with another count would wait for registers forever.
-  static const int regs = [&] {
-    cudaFuncAttributes a;
-    return cudaFuncGetAttributes(&a, kern) == cudaSuccess ? a.numRegs : 0;
-  }();
-  if (regs != C::REGS_LAUNCH) return B200ATTN_ERR_UNSUPPORTED;
+  static std::atomic<uint64_t> done{0};
+  const int rc = prepare_kernel(reinterpret_cast<const void*>(kern), C::SMEM, C::REGS_LAUNCH, device, done);
+  if (rc != B200ATTN_OK) return rc;
   const int blocks = sm_count < b200p::kChMaxBlocks ? sm_count : b200p::kChMaxBlocks;
   kern<<<blocks, C::THREADS, C::SMEM, st>>>(tq, tk, tv, p, codes);
   if (cudaGetLastError() != cudaSuccess) return B200ATTN_ERR_CUDA;
@@ -241,8 +266,8 @@ int b200attn_paged_slots(int* block_table, size_t table_stride, int table_width,
   for (const void* p : ptrs)
     if (!aligned(p, 4)) return B200ATTN_ERR_INVALID;
   if (batch > b200p::kSlotsMaxBatch || total >= (1 << 30) || table_stride > 0x7fffffff) return B200ATTN_ERR_UNSUPPORTED;
-  int sm_count = 0;
-  const int rc = device_ok(&sm_count);
+  int sm_count = 0, device = 0;
+  const int rc = device_ok(&sm_count, &device);
   if (rc != B200ATTN_OK) return rc;
 
   b200p::PagedSlots p = {};
@@ -262,13 +287,14 @@ int b200attn_paged_slots(int* block_table, size_t table_stride, int table_width,
   p.kv = kv_lens;
   p.pos = positions;
   p.slot = slots;
-  const int smem = 2 * (batch + 1) * static_cast<int>(sizeof(int));
-  if (smem > 48 * 1024 - 1024 &&
-      cudaFuncSetAttribute(b200p::paged_slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return B200ATTN_ERR_CUDA;
+  const int smem = (3 * batch + 2) * static_cast<int>(sizeof(int));
+  static std::atomic<uint64_t> done{0};
+  const int prc = prepare_kernel(reinterpret_cast<const void*>(b200p::paged_slots_kernel),
+                                 (3 * b200p::kSlotsMaxBatch + 2) * static_cast<int>(sizeof(int)), 0, device, done);
+  if (prc != B200ATTN_OK) return prc;
   // One cluster: its barrier stands between reading the free list's head and
   // writing it. A step that one block covers in a pass or two takes one block.
-  const int blocks = total <= 2 * b200p::kSlotsThreads ? 1 : b200p::kSlotsCluster;
+  const int blocks = total <= b200p::kSlotsThreads ? 1 : b200p::kSlotsCluster;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks, 1, 1);
   cfg.blockDim = dim3(b200p::kSlotsThreads, 1, 1);
@@ -297,8 +323,8 @@ int b200attn_paged_append(const void* k, const void* v, size_t k_stride, size_t 
   const int64_t units =
       static_cast<int64_t>(total) * cache->Hkv * ((cache->d_qk + cache->d_v) / b200p::kAppendUnit);
   if (units >= (int64_t(1) << 31)) return B200ATTN_ERR_UNSUPPORTED;
-  int sm_count = 0;
-  const int rc = device_ok(&sm_count);
+  int sm_count = 0, device = 0;
+  const int rc = device_ok(&sm_count, &device);
   if (rc != B200ATTN_OK) return rc;
 
   b200p::PagedAppend p = {};
@@ -319,17 +345,16 @@ int b200attn_paged_append(const void* k, const void* v, size_t k_stride, size_t 
   p.slots = slots;
   p.T = total;
   p.H = cache->Hkv;
-  p.d[0] = cache->d_qk;
-  p.d[1] = cache->d_v;
   p.num_pages = cache->num_pages;
-  p.page_size = cache->page_size;
+  p.page_size = b200p::fast_div(cache->page_size);
+  p.per_token = b200p::fast_div(cache->Hkv * ((cache->d_qk + cache->d_v) / b200p::kAppendUnit));
   const int64_t want = (units + b200p::kAppendThreads - 1) / b200p::kAppendThreads;
   const int blocks = static_cast<int>(want < 8 * sm_count ? want : 8 * sm_count);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cache->dtype == B200ATTN_BF16)
-    b200p::paged_append_kernel<false><<<blocks, b200p::kAppendThreads, 0, st>>>(p);
-  else
-    b200p::paged_append_kernel<true><<<blocks, b200p::kAppendThreads, 0, st>>>(p);
+  auto kern = cache->dtype == B200ATTN_BF16
+                  ? (cache->d_qk == 128 ? b200p::paged_append_kernel<128, 128, false> : b200p::paged_append_kernel<192, 128, false>)
+                  : (cache->d_qk == 128 ? b200p::paged_append_kernel<128, 128, true> : b200p::paged_append_kernel<192, 128, true>);
+  kern<<<blocks, b200p::kAppendThreads, 0, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? B200ATTN_OK : B200ATTN_ERR_CUDA;
 }
 
@@ -363,8 +388,8 @@ int b200attn_paged_fwd(const void* q, size_t q_stride, const b200attn_paged_cach
     return B200ATTN_ERR_UNSUPPORTED;
   const size_t need = b200attn_paged_fwd_workspace_bytes(total, max_seqlen_q, Hq, cache->Hkv);
   if (!workspace || workspace_bytes < need || !aligned(workspace, 16)) return B200ATTN_ERR_WORKSPACE;
-  int sm_count = 0;
-  const int rc = device_ok(&sm_count);
+  int sm_count = 0, device = 0;
+  const int rc = device_ok(&sm_count, &device);
   if (rc != B200ATTN_OK) return rc;
 
   const bool fp8 = cache->dtype == B200ATTN_FP8_E4M3;
@@ -402,16 +427,16 @@ int b200attn_paged_fwd(const void* q, size_t q_stride, const b200attn_paged_cach
   p.part_o = reinterpret_cast<float*>(ws + w.o);
   if (few) {
     if (cache->d_qk == 128)
-      return fp8 ? launch_few<128, true>(cache, p, sm_count, st) : launch_few<128, false>(cache, p, sm_count, st);
-    return fp8 ? launch_few<192, true>(cache, p, sm_count, st) : launch_few<192, false>(cache, p, sm_count, st);
+      return fp8 ? launch_few<128, true>(cache, p, sm_count, device, st) : launch_few<128, false>(cache, p, sm_count, device, st);
+    return fp8 ? launch_few<192, true>(cache, p, sm_count, device, st) : launch_few<192, false>(cache, p, sm_count, device, st);
   }
   // key blocks of all units, counted in 32 bits
   const int64_t pairs = static_cast<int64_t>(total) / (2 * (b200p::kChM / G)) + batch;
   if (pairs * cache->Hkv >= (int64_t(1) << 31) || pairs * cache->Hkv * (keys / b200p::kChN + 1) >= (int64_t(1) << 31))
     return B200ATTN_ERR_UNSUPPORTED;
   if (cache->d_qk == 128)
-    return fp8 ? launch_chunk<128, true>(cache, p, sm_count, st) : launch_chunk<128, false>(cache, p, sm_count, st);
-  return fp8 ? launch_chunk<192, true>(cache, p, sm_count, st) : launch_chunk<192, false>(cache, p, sm_count, st);
+    return fp8 ? launch_chunk<128, true>(cache, p, sm_count, device, st) : launch_chunk<128, false>(cache, p, sm_count, device, st);
+  return fp8 ? launch_chunk<192, true>(cache, p, sm_count, device, st) : launch_chunk<192, false>(cache, p, sm_count, device, st);
 }
 
 }  // extern "C"

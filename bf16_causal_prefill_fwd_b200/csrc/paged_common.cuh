@@ -104,6 +104,23 @@ __device__ __forceinline__ float fast_log2(float x) {
   return y;
 }
 
+// n / d for 0 <= n < 2^31 by a multiplication: with l = ceil(log2 d) and m =
+// ceil(2^(31 + l) / d), n m / 2^(31 + l) exceeds n / d by less than 1 / d, so the
+// floors agree (Granlund and Montgomery, "Division by invariant integers using
+// multiplication", 1994).
+struct FastDiv {
+  uint32_t d, m, s;
+};
+inline FastDiv fast_div(uint32_t d) {
+  uint32_t l = 0;
+  while ((uint64_t(1) << l) < d) ++l;
+  if (l == 0) return {1, 0, 0};  // d = 1: taken apart in the division
+  return {d, static_cast<uint32_t>(((uint64_t(1) << (31 + l)) + d - 1) / d), l - 1};
+}
+__device__ __forceinline__ uint32_t operator/(uint32_t n, const FastDiv& f) {
+  return f.m == 0 ? n : __umulhi(n, f.m) >> f.s;
+}
+
 // What the attention kernels are given. Strides are in elements.
 struct PagedAttn {
   const __nv_bfloat16* q;  // [T, Hq, d_qk], rows of one token contiguous

@@ -39,8 +39,7 @@ namespace b200p {
 constexpr int kDecKeys = 64;     // keys per tile (one stage of the ring)
 constexpr int kDecWarps = 4;     // consumer warps, 16 keys of a tile each
 constexpr int kDecThreads = 32 * (kDecWarps + 1);
-constexpr int kDecBlocksPerSm = 2;
-constexpr int kDecMaxBlocks = 320;  // workspace slots are sized for this many blocks
+constexpr int kDecMaxBlocks = 480;  // workspace slots are sized for this many blocks
 constexpr int kDecMaxRows = 16;
 
 template <int DQK, int DV, bool FP8, int NT>
@@ -55,7 +54,10 @@ struct DecCfg {
   static constexpr int MERGE = kDecWarps * 8 * MROW * 4;  // O of the four warps, eight rows at a time
   static constexpr int ML = kDecWarps * 8 * 2 * 4;      // their (m, l)
   static constexpr int FIXED = MERGE + ML + 512 /*barriers, plan*/ + 1024 /*alignment*/;
-  static constexpr int BUDGET = 113 * 1024;  // two blocks per SM
+  // Blocks per SM. Two are enough to stream bf16 pages; with e4m3 a tile is half
+  // the bytes for more instructions, and a third block's warps fill the gaps.
+  static constexpr int BLOCKS = FP8 && NT == 1 ? 3 : 2;
+  static constexpr int BUDGET = 227 * 1024 / BLOCKS / 1024 * 1024 - (BLOCKS == 2 ? 0 : 1024);
   static constexpr int FIT = (BUDGET - FIXED) / STAGE;
   static constexpr int STAGES = FIT > 6 ? 6 : FIT;
   static constexpr int SMEM = STAGES * STAGE + FIXED;
@@ -175,7 +177,7 @@ struct DecWalk {
 };
 
 template <int DQK, int DV, bool FP8, int NT>
-__global__ void __launch_bounds__(kDecThreads, kDecBlocksPerSm)
+__global__ void __launch_bounds__(kDecThreads, DecCfg<DQK, DV, FP8, NT>::BLOCKS)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         const PagedAttn p) {
   using C = DecCfg<DQK, DV, FP8, NT>;
@@ -518,32 +520,70 @@ __global__ void __launch_bounds__(kDecThreads, kDecBlocksPerSm)
   }
 }
 
-// Joins the parts of the units that several blocks have worked on: block c
-// takes the unit that begins, but does not end, in block c. Parts are added in
-// block order. Rows are spread over gridDim.y.
+// Joins the parts of the units that several blocks have worked on: block c of
+// the grid takes the unit that begins, but does not end, in block c; its rows
+// are spread over gridDim.y. O = sum_b 2^(m_b - M) O_b / sum_b 2^(m_b - M) l_b.
+// A row may have hundreds of parts (one long request over the whole GPU), so
+// its parts are read side by side: lane i of every warp has (m, l) of part i,
+// the four warps add every fourth part's O (16 bytes per lane, several loads in
+// flight), and their sums meet in shared memory. The order is fixed.
 template <int DV>
-__global__ void __launch_bounds__(DV) paged_join_kernel(const PagedAttn p) {
+__global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttn p) {
+  static_assert(DV == 128, "a warp reads a row of O with 16 bytes per lane");
+  __shared__ float s_o[4][DV];
   pdl_wait();
-  const int c = blockIdx.x, td = threadIdx.x;
+  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const PartDesc e = reinterpret_cast<const PartDesc*>(p.desc)[c];
   if (e.last < 0) return;
+  const int parts = e.last - c + 1;
+  // part i: the tail slot of the first block, then the head slots of the next ones
+  auto slot_row = [&](int i, int r) {
+    return static_cast<int64_t>(2 * (c + i) + (i == 0 ? 1 : 0)) * p.slot_rows + r;
+  };
   for (int r = blockIdx.y; r < e.nrows; r += gridDim.y) {
-    float mm = -INFINITY, ll = 0.0f, acc = 0.0f;
-    for (int b = c; b <= e.last; ++b) {
-      const int64_t at = static_cast<int64_t>(2 * b + (b == c ? 1 : 0)) * p.slot_rows + r;
-      const float m = p.part_ml[2 * at], l = p.part_ml[2 * at + 1];
-      if (l == 0.0f) continue;  // this part saw none of the row's keys
-      const float mn = fmaxf(mm, m);
-      const float f0 = ex2_approx(mm - mn), f1 = ex2_approx(m - mn);
-      acc = fmaf(acc, f0, p.part_o[at * DV + td] * f1);
-      ll = fmaf(ll, f0, l * f1);
-      mm = mn;
+    float mm = -INFINITY;
+    for (int i = lane; i < parts; i += 32) {
+      const float2 x = *reinterpret_cast<const float2*>(p.part_ml + 2 * slot_row(i, r));
+      if (x.y != 0.0f) mm = fmaxf(mm, x.x);  // a part with l = 0 saw none of the row's keys
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+    float ll = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+      float f = 0.0f;
+      if (i0 + lane < parts) {
+        const float2 x = *reinterpret_cast<const float2*>(p.part_ml + 2 * slot_row(i0 + lane, r));
+        if (x.y != 0.0f) {
+          f = ex2_approx(x.x - mm);
+          ll = fmaf(x.y, f, ll);
+        }
+      }
+      const int n = min(32, parts - i0);
+#pragma unroll 4
+      for (int i = warp; i < n; i += 4) {
+        const float w = __shfl_sync(0xffffffffu, f, i);
+        const float4 o = *reinterpret_cast<const float4*>(p.part_o + slot_row(i0 + i, r) * DV + 4 * lane);
+        if (w != 0.0f) {  // a part without keys may have left O unwritten
+          acc.x = fmaf(o.x, w, acc.x);
+          acc.y = fmaf(o.y, w, acc.y);
+          acc.z = fmaf(o.z, w, acc.z);
+          acc.w = fmaf(o.w, w, acc.w);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, o);
+    *reinterpret_cast<float4*>(&s_o[warp][4 * lane]) = acc;
+    __syncthreads();
     const int row = e.row0 + r, tok = row / p.G, hq = e.hkv * p.G + row - tok * p.G;
+    const int td = threadIdx.x;
+    const float sum = (s_o[0][td] + s_o[1][td]) + (s_o[2][td] + s_o[3][td]);
     const float inv = ll == 0.0f ? 0.0f : (p.v_scale != nullptr ? __ldg(p.v_scale + e.hkv) : 1.0f) / ll;
-    p.o[(static_cast<int64_t>(e.t0 + tok) * p.Hq + hq) * DV + td] = __float2bfloat16(acc * inv);
+    p.o[(static_cast<int64_t>(e.t0 + tok) * p.Hq + hq) * DV + td] = __float2bfloat16(sum * inv);
     if (p.lse != nullptr && td == 0)
       p.lse[static_cast<int64_t>(hq) * p.T + e.t0 + tok] = ll == 0.0f ? -INFINITY : (mm + fast_log2(ll)) * kLn2;
+    __syncthreads();  // s_o is written again
   }
 }
 

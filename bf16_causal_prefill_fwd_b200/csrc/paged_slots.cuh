@@ -25,9 +25,9 @@
 
 namespace b200p {
 
-constexpr int kSlotsThreads = 512;
+constexpr int kSlotsThreads = 1024;
 constexpr int kSlotsCluster = 8;
-constexpr int kSlotsMaxBatch = 16384;  // two prefix arrays in shared memory
+constexpr int kSlotsMaxBatch = 16384;  // three arrays in shared memory
 
 struct PagedSlots {
   int* table;
@@ -63,6 +63,7 @@ __global__ void __launch_bounds__(kSlotsThreads) paged_slots_kernel(const PagedS
   extern __shared__ int sm[];
   int* s_cu = sm;               // [B + 1]
   int* s_fr = sm + (p.B + 1);   // [B + 1]
+  int* s_ctx = s_fr + (p.B + 1);  // [B]
   __shared__ int2 warp_sum[kSlotsThreads / 32];
   __shared__ int s_bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -81,6 +82,7 @@ __global__ void __launch_bounds__(kSlotsThreads) paged_slots_kernel(const PagedS
     int n = 0, fresh = 0;
     if (b < p.B) {
       const int c = __ldg(p.ctx + b);
+      s_ctx[b] = c;
       n = __ldg(p.nw + b);
       const int64_t want = (static_cast<int64_t>(c) + n + ps - 1) / ps;
       if (c < 0 || n < 0 || n > p.total || want > p.width) {
@@ -131,21 +133,22 @@ __global__ void __launch_bounds__(kSlotsThreads) paged_slots_kernel(const PagedS
   const int used = bad ? 0 : run.x;
   for (int b = at; b <= p.B; b += step) {
     p.cu[b] = bad ? 0 : s_cu[b];
-    if (b < p.B) p.kv[b] = bad ? 0 : __ldg(p.ctx + b) + s_cu[b + 1] - s_cu[b];
+    if (b < p.B) p.kv[b] = bad ? 0 : s_ctx[b] + s_cu[b + 1] - s_cu[b];
   }
   if (alloc && !bad) {
     for (int j = at; j < run.y; j += step) {
       const int b = last_not_above(s_fr, p.B, j);
-      const int held = (__ldg(p.ctx + b) + ps - 1) / ps;
+      const int held = (s_ctx[b] + ps - 1) / ps;
       p.table[b * p.table_stride + held + (j - s_fr[b])] = __ldg(p.free_pages + head + j);
     }
   }
   if (alloc && rank == 0 && tid == 0) *p.head_out = head + (bad ? 0 : run.y);
+#pragma unroll 2
   for (int t = at; t < p.total; t += step) {
     int pos = 0, slot = -1;
     if (t < used) {
       const int b = last_not_above(s_cu, p.B, t);
-      const int c = __ldg(p.ctx + b);
+      const int c = s_ctx[b];
       pos = c + t - s_cu[b];
       const int idx = pos / ps, held = (c + ps - 1) / ps;
       const int page = alloc && idx >= held ? __ldg(p.free_pages + head + s_fr[b] + idx - held)
