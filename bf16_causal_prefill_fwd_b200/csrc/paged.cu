@@ -112,10 +112,11 @@ int check_cache(const b200attn_paged_cache* c) {
   return B200ATTN_OK;
 }
 
-// A cache tensor as a 4-D map {d, head, row of the page, page} with a box of 128
-// bytes of one head of `rows` rows, 128-byte swizzle; out of range reads zero.
+// A cache tensor as a 4-D map {d, head, row of the page, page} with a box of one
+// head of `rows` rows: 128 bytes of each with the 128-byte swizzle, or (swizzle
+// false) whole rows as they are; out of range reads zero.
 bool page_map(CUtensorMap* m, const void* ptr, bool fp8, int d, int H, int ps, int pages, int64_t head, int64_t token,
-              int64_t page, int rows) {
+              int64_t page, int rows, bool swizzle) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   const cuuint64_t esz = fp8 ? 1 : 2;
@@ -124,19 +125,20 @@ bool page_map(CUtensorMap* m, const void* ptr, bool fp8, int d, int H, int ps, i
                    sp = pages > 1 ? page * esz : d * esz;
   const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)ps, (cuuint64_t)pages};
   const cuuint64_t strides[3] = {sh, st, sp};
-  const cuuint32_t box[4] = {(cuuint32_t)(128 / esz), 1, (cuuint32_t)rows, 1};
+  const cuuint32_t box[4] = {swizzle ? (cuuint32_t)(128 / esz) : (cuuint32_t)d, 1, (cuuint32_t)rows, 1};
   const cuuint32_t one[4] = {1, 1, 1, 1};
   return enc(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr),
-             dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool page_maps(CUtensorMap* tk, CUtensorMap* tv, const b200attn_paged_cache* c, int rows) {
+bool page_maps(CUtensorMap* tk, CUtensorMap* tv, const b200attn_paged_cache* c, int rows, bool swizzle) {
   const bool fp8 = c->dtype == B200ATTN_FP8_E4M3;
   return page_map(tk, c->k, fp8, c->d_qk, c->Hkv, c->page_size, c->num_pages, c->k_head_stride, c->k_token_stride,
-                  c->k_page_stride, rows) &&
+                  c->k_page_stride, rows, swizzle) &&
          page_map(tv, c->v, fp8, c->d_v, c->Hkv, c->page_size, c->num_pages, c->v_head_stride, c->v_token_stride,
-                  c->v_page_stride, rows);
+                  c->v_page_stride, rows, swizzle);
 }
 
 // Launch whose blocks may be scheduled while the kernel before it drains (that
@@ -179,7 +181,7 @@ int launch_decode(const b200attn_paged_cache* c, PagedAttn p, int sm_count, int 
   p.box = gcd(p.page_size, b200p::kDecKeys);
   p.slot_rows = b200p::kDecMaxRows;
   CUtensorMap tk, tv;
-  if (!page_maps(&tk, &tv, c, p.box)) return B200ATTN_ERR_CUDA;
+  if (!page_maps(&tk, &tv, c, p.box, true)) return B200ATTN_ERR_CUDA;
   auto kern = b200p::paged_decode_kernel<DQK, 128, FP8, NT>;
   static std::atomic<uint64_t> done{0};
   const int rc = prepare_kernel(reinterpret_cast<const void*>(kern), C::SMEM, 0, device, done);
@@ -210,13 +212,7 @@ int launch_chunk(const b200attn_paged_cache* c, PagedAttn p, int sm_count, int d
   p.box = gcd(p.page_size, b200p::kChN);
   p.slot_rows = chunk_rows(p.T, p.G);
   CUtensorMap tq = {}, tk = {}, tv = {};
-  b200p::ChCodes codes = {};
-  if (FP8) {
-    codes = {{static_cast<const uint8_t*>(c->k), static_cast<const uint8_t*>(c->v)},
-             {c->k_page_stride, c->v_page_stride},
-             {c->k_token_stride, c->v_token_stride},
-             {c->k_head_stride, c->v_head_stride}};
-  } else {
+  if (!FP8) {
     // {d, head, token} with a box of 64 columns, the G heads of a group and a tile's tokens
     const cuuint64_t dims[3] = {DQK, (cuuint64_t)p.Hq, (cuuint64_t)p.T};
     const cuuint64_t strides[2] = {DQK * 2, (cuuint64_t)(p.T > 1 ? p.q_stride : static_cast<int64_t>(p.Hq) * DQK) * 2};
@@ -227,16 +223,16 @@ int launch_chunk(const b200attn_paged_cache* c, PagedAttn p, int sm_count, int d
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return B200ATTN_ERR_CUDA;
-    if (!page_maps(&tk, &tv, c, p.box)) return B200ATTN_ERR_CUDA;
   }
+  if (!page_maps(&tk, &tv, c, p.box, !FP8)) return B200ATTN_ERR_CUDA;
   auto kern = b200p::paged_chunk_kernel<DQK, 128, FP8>;
   static std::atomic<uint64_t> done{0};
   const int rc = prepare_kernel(reinterpret_cast<const void*>(kern), C::SMEM, C::REGS_LAUNCH, device, done);
   if (rc != B200ATTN_OK) return rc;
   const int blocks = sm_count < b200p::kChMaxBlocks ? sm_count : b200p::kChMaxBlocks;
-  kern<<<blocks, C::THREADS, C::SMEM, st>>>(tq, tk, tv, p, codes);
+  kern<<<blocks, C::THREADS, C::SMEM, st>>>(tq, tk, tv, p);
   if (cudaGetLastError() != cudaSuccess) return B200ATTN_ERR_CUDA;
-  return launch_dependent(b200p::paged_join_kernel<128>, dim3(blocks, 32, 1), 128, st, static_cast<const PagedAttn>(p));
+  return launch_dependent(b200p::paged_join_kernel<128>, dim3(blocks, p.slot_rows < 64 ? (p.slot_rows + 3) / 4 : 16, 1), 128, st, static_cast<const PagedAttn>(p));
 }
 
 }  // namespace
@@ -432,7 +428,7 @@ int b200attn_paged_fwd(const void* q, size_t q_stride, const b200attn_paged_cach
   }
   // key blocks of all units, counted in 32 bits
   const int64_t pairs = static_cast<int64_t>(total) / (2 * (b200p::kChM / G)) + batch;
-  if (pairs * cache->Hkv >= (int64_t(1) << 31) || pairs * cache->Hkv * (keys / b200p::kChN + 1) >= (int64_t(1) << 31))
+  if (pairs * cache->Hkv >= (int64_t(1) << 31) || pairs * cache->Hkv * (keys / b200p::kChN + 1 + b200p::kChUnitCost) >= (int64_t(1) << 31))
     return B200ATTN_ERR_UNSUPPORTED;
   if (cache->d_qk == 128)
     return fp8 ? launch_chunk<128, true>(cache, p, sm_count, device, st) : launch_chunk<128, false>(cache, p, sm_count, device, st);

@@ -14,8 +14,8 @@
 // {64 columns, G heads, tokens} lays the rows out so.
 //
 // Split. A unit is (request, key/value head, pair of row tiles) and runs over
-// its key blocks of 128. The blocks of all units form one line that is cut into
-// equal runs, one per SM: a step of few units still uses every SM, and no SM
+// its key blocks of 128. The blocks of all units (and a fixed cost per unit) form
+// one line that is cut into equal runs, one per SM: a step of few units still uses every SM, and no SM
 // waits for a longer unit. A unit cut by a run's end leaves (m, l, O) per part,
 // joined in block order by paged_join_kernel. Every block finds its run from
 // the lengths in device memory.
@@ -24,11 +24,12 @@
 // (TMA, 128-byte swizzle; pages behind the last are read as zeros through an
 // out-of-range page number). The rows behind the last key inside its page may
 // hold anything, and 0 * NaN is NaN, so the V warp clears them in shared memory
-// before the tensor core reads them; scores are replaced by select. e4m3: four
-// more warps read the codes (each 16-key group lies in one page), turn them into
-// fp16 exactly and write the swizzled tiles; they hold the next block's codes
-// in registers while they convert this one's, so the cache's latency is hidden.
-// Q then becomes fp16 too, after a power of two per row.
+// before the tensor core reads them; scores are replaced by select. e4m3: the same
+// warps copy the codes of a block to a staging tile, and four more warps turn
+// them into fp16 exactly and write the swizzled tiles (about 20 instructions
+// per 16 codes, beside the softmax's eight warps); the staging tile is free for
+// the next block as soon as they hold it in registers. Q becomes fp16 too, after
+// a power of two per row.
 //
 // Bound by the tensor core (2 x 2 x 128^3 products per key block and pair) and,
 // for chunks of a few tokens, by reading the cache.
@@ -41,6 +42,10 @@ namespace b200p {
 constexpr int kChM = 128;  // rows per tile
 constexpr int kChN = 128;  // keys per block
 constexpr int kChRows = 2 * kChM;
+// What a unit costs beyond its key blocks (its Q, the pipeline's filling, its
+// output), in key blocks: counted in when the line is cut, so that a run of many
+// short units is not longer than one of few long ones.
+constexpr int kChUnitCost = 2;
 constexpr int kChMaxBlocks = 160;  // workspace slots are sized for this many blocks
 
 template <int DQK, int DV, bool FP8>
@@ -49,20 +54,21 @@ struct ChCfg {
   static constexpr int REGS_LAUNCH = FP8 ? 128 : 168;
   // Register split by warpgroup: control, converters (e4m3), softmax. The sums
   // stay within what the block was launched with.
-  static constexpr int REGS_CTRL = FP8 ? 56 : 72;
-  static constexpr int REGS_CONV = 104;
+  static constexpr int REGS_CTRL = 72;
+  static constexpr int REGS_CONV = 88;
   static constexpr int REGS_SOFT = FP8 ? 176 : 208;
   static_assert(128 * REGS_CTRL + (FP8 ? 128 * REGS_CONV : 0) + 256 * REGS_SOFT <= THREADS * REGS_LAUNCH, "registers");
   static constexpr int CHUNK = kChM * 128;  // 128 rows x 128 bytes, swizzled
   static constexpr int QK_CHUNKS = DQK / 64, V_CHUNKS = DV / 64;
   static constexpr int Q_BYTES = QK_CHUNKS * CHUNK, K_BYTES = QK_CHUNKS * CHUNK, V_BYTES = V_CHUNKS * CHUNK;
-  static constexpr int AVAIL = 227 * 1024 - 2048 - 2 * Q_BYTES;
+  static constexpr int KC_BYTES = FP8 ? kChN * DQK : 0, VC_BYTES = FP8 ? kChN * DV : 0;  // staged codes
+  static constexpr int AVAIL = 227 * 1024 - 2048 - 2 * Q_BYTES - KC_BYTES - VC_BYTES;
   static constexpr int PAIRS = AVAIL / (K_BYTES + V_BYTES);
   static constexpr int SV = PAIRS >= 2 ? 2 : 1;
   static constexpr int SK = (AVAIL - SV * V_BYTES) / K_BYTES > 3 ? 3 : (AVAIL - SV * V_BYTES) / K_BYTES;
-  static constexpr int BARS = 2 + 2 + 2 * SK + 2 * SV + 1 + 2 + 1 + 2 + 2 + 2 + 2 + 2;
-  static constexpr int SMEM = 2 * Q_BYTES + SK * K_BYTES + SV * V_BYTES + 1024 + 1024;
-  static_assert(8 * BARS + 64 <= 1024 && SMEM <= 227 * 1024 && SK >= 2, "shared memory");
+  static constexpr int BARS = 2 + 2 + 2 * SK + 2 * SV + 1 + 4 + 2 + 1 + 2 + 2 + 2 + 2 + 2;
+  static constexpr int SMEM = 2 * Q_BYTES + SK * K_BYTES + SV * V_BYTES + KC_BYTES + VC_BYTES + 1024 + 1024;
+  static_assert(8 * BARS + 8 <= 512 && 512 + 8 * 64 <= 1024 && SMEM <= 227 * 1024 && SK >= 1, "shared memory");
   // Tensor memory: S [0, 128) for both tiles in turn, O_t at 128 + 128 t, P_t
   // (16-bit, 64 columns) at 384 + 64 t.
   static constexpr int TM_O = 128, TM_P = 384;
@@ -91,18 +97,24 @@ __device__ __forceinline__ int ch_pair_blocks(const Request& r, int p, int tpt, 
 
 __device__ __forceinline__ int ch_pairs(const Request& r, int tpt) { return (r.nq + 2 * tpt - 1) / (2 * tpt); }
 
-// Key blocks of one key/value head of a request.
-__device__ __forceinline__ int ch_head_blocks(const Request& r, int tpt, int causal) {
+// Length in the line of the units of one key/value head of a request.
+__device__ __forceinline__ int ch_head_cost(const Request& r, int tpt, int causal) {
   const int n = ch_pairs(r, tpt);
   if (n == 0) return 0;
-  if (!causal) return n * ch_pair_blocks(r, 0, tpt, causal);
-  int s = 0;
+  if (!causal) return n * (ch_pair_blocks(r, 0, tpt, causal) + kChUnitCost);
+  int s = n * kChUnitCost;
   for (int p = 0; p < n; ++p) s += ch_pair_blocks(r, p, tpt, causal);
   return s;
 }
 
+__device__ __forceinline__ void ld_shared_v4(uint32_t addr, int& a, int& b, int& c, int& d) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(addr) : "memory");
+}
+
+// A block's run: it starts `skip` into unit (b, h, pair), is `count` long, and
+// `first` is its place in the line; runs are `per` long.
 struct ChStart {
-  int b, h, pair, k0, count, first, per;
+  int b, h, pair, skip, count, first, per;
 };
 
 // A block's run of the line. Every thread of the block; `sm`: THREADS + 8 ints.
@@ -112,7 +124,7 @@ __device__ __forceinline__ ChStart ch_start(const PagedAttn& p, int tpt, int* sm
   const int seg = (p.B + THREADS - 1) / THREADS;
   const int b0 = min(tid * seg, p.B), b1 = min(b0 + seg, p.B);
   int sum = 0;
-  for (int b = b0; b < b1; ++b) sum += ch_head_blocks(paged_request(p, b, blockIdx.x == 0), tpt, p.causal);
+  for (int b = b0; b < b1; ++b) sum += ch_head_cost(paged_request(p, b, blockIdx.x == 0), tpt, p.causal);
   sm[tid] = sum;
   __syncthreads();
   if (tid < 32) {
@@ -144,10 +156,10 @@ __device__ __forceinline__ ChStart ch_start(const PagedAttn& p, int tpt, int* sm
     if (acc <= d.first && d.first < acc + sum * p.Hkv) {
       for (int b = b0; b < b1; ++b) {
         const Request r = paged_request(p, b, false);
-        const int n = ch_head_blocks(r, tpt, p.causal);
+        const int n = ch_head_cost(r, tpt, p.causal);
         if (d.first < acc + n * p.Hkv) {
           int at = (d.first - acc) % n, pair = 0;
-          for (int m; at >= (m = ch_pair_blocks(r, pair, tpt, p.causal)); ++pair) at -= m;
+          for (int m; at >= (m = ch_pair_blocks(r, pair, tpt, p.causal) + kChUnitCost); ++pair) at -= m;
           sm[THREADS + 1] = b;
           sm[THREADS + 2] = (d.first - acc) / n;
           sm[THREADS + 3] = pair;
@@ -162,59 +174,77 @@ __device__ __forceinline__ ChStart ch_start(const PagedAttn& p, int tpt, int* sm
   d.b = sm[THREADS + 1];
   d.h = sm[THREADS + 2];
   d.pair = sm[THREADS + 3];
-  d.k0 = sm[THREADS + 4];
+  d.skip = sm[THREADS + 4];
   return d;
 }
 
 // Walks the pieces of a block's run: key blocks [kb, ke) of unit (b, h, pair).
+// A unit takes kChUnitCost + (its key blocks) of the line, the cost first.
 struct ChWalk {
   const PagedAttn& p;
   Request r;
   int b, h, pair, tpt;
   int kb, ke, n0, n1;  // this piece; key blocks of the unit's tiles
-  int left, at;        // blocks after this piece; the piece's place in the line
+  int left, at;        // what is left of the run after this piece; the unit's place in the line
   __device__ ChWalk(const PagedAttn& params, const ChStart& d, int tokens) : p(params), tpt(tokens) {
     b = d.b;
     h = d.h;
     pair = d.pair;
     left = d.count;
-    at = d.first;
-    kb = d.k0;
-    ke = kb;
+    at = d.first - d.skip;
+    kb = ke = n0 = n1 = 0;
     if (left > 0) {
       r = paged_request(p, b, false);
-      take();
+      take(d.skip);
+      if (!valid()) next();
     }
   }
-  __device__ void take() {
+  // The softmax warps keep a whole score row in registers; what the walk needs
+  // is put into shared memory (64 bytes per warp, every lane the same) while the
+  // keys of a piece go by.
+  __device__ void put(uint32_t at_smem) const {
+    st_shared_v4(at_smem, b, h, pair, left);
+    st_shared_v4(at_smem + 16, at, kb, ke, n0);
+    st_shared_v4(at_smem + 32, n1, r.t0, r.nq, r.kv);
+  }
+  __device__ void get(uint32_t at_smem) {
+    ld_shared_v4(at_smem, b, h, pair, left);
+    ld_shared_v4(at_smem + 16, at, kb, ke, n0);
+    ld_shared_v4(at_smem + 32, n1, r.t0, r.nq, r.kv);
+  }
+  __device__ void take(int skip) {
     n0 = ch_blocks(r, 2 * pair, tpt, p.causal);
     n1 = ch_blocks(r, 2 * pair + 1, tpt, p.causal);
-    const int n = min(left, max(n0, n1) - kb);
-    ke = kb + n;
+    const int n = min(left, max(n0, n1) + kChUnitCost - skip);
+    kb = max(0, skip - kChUnitCost);
+    ke = max(0, skip + n - kChUnitCost);
     left -= n;
   }
   __device__ bool valid() const { return ke > kb; }
   __device__ int end(int t) const { return min(ke, t ? n1 : n0); }      // tile t runs blocks [kb, end(t))
   __device__ bool has(int t) const { return end(t) > kb; }
   __device__ bool whole() const { return kb == 0 && ke == max(n0, n1); }
+  __device__ int last() const { return at + kChUnitCost + max(n0, n1) - 1; }  // place of the unit's last key block
   __device__ void next() {
-    at += ke - kb;
-    kb = ke = 0;
-    if (left == 0) return;
-    if (++pair == ch_pairs(r, tpt)) {
-      pair = 0;
-      if (++h == p.Hkv) {
-        h = 0;
-        do {  // more blocks are left, so a request with tokens follows
-          if (++b >= p.B) {
-            left = 0;
-            return;
-          }
-          r = paged_request(p, b, false);
-        } while (r.nq == 0);
+    do {
+      at += max(n0, n1) + kChUnitCost;
+      kb = ke = 0;
+      if (left == 0) return;
+      if (++pair == ch_pairs(r, tpt)) {
+        pair = 0;
+        if (++h == p.Hkv) {
+          h = 0;
+          do {  // more is left, so a request with tokens follows
+            if (++b >= p.B) {
+              left = 0;
+              return;
+            }
+            r = paged_request(p, b, false);
+          } while (r.nq == 0);
+        }
       }
-    }
-    take();
+      take(0);
+    } while (!valid());  // the run's end may hold no more than a unit's cost
   }
 };
 
@@ -249,51 +279,36 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, 
       : "memory");
 }
 
-// e4m3 caches: what the converting warps read codes from (strides in bytes).
-struct ChCodes {
-  const uint8_t* base[2];
-  int64_t page[2], token[2], head[2];
-};
-
-// One block of 128 keys of K or V as codes in registers: thread `tid` of 128
-// holds, of each 32 keys, units tid, tid + 128, ... (16 codes each, D / 16 to a row).
+// One staged block of 128 keys of K or V: thread `tid` of 128 takes, of each 32
+// keys, units tid, tid + 128, ... (16 codes each, D / 16 to a row).
 template <int D>
 struct ChRegs {
   static constexpr int UPR = D / 16, PER = 32 * UPR / 128;
   uint4 c[4][PER];
-  __device__ __forceinline__ void load(const ChCodes& s, int which, int h, int kv0, int kv, int pages, int ps,
-                                       int num_pages, int tid) {
+  __device__ __forceinline__ void load(const uint4* staged, int tid) {
 #pragma unroll
     for (int g = 0; g < 4; ++g)
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int idx = i * 128 + tid, row = idx / UPR, u = idx - row * UPR;
-        const int key = kv0 + 32 * g + row;
-        const int page = __shfl_sync(0xffffffffu, pages, 2 * g + (row >> 4));
-        c[g][i] = make_uint4(0, 0, 0, 0);
-        if (key < kv && page < num_pages)
-          c[g][i] = __ldg(reinterpret_cast<const uint4*>(s.base[which] + page * s.page[which] +
-                                                         (key % ps) * s.token[which] + h * s.head[which] + u * 16));
-      }
+      for (int i = 0; i < PER; ++i) c[g][i] = staged[g * 32 * UPR + i * 128 + tid];
   }
-  __device__ __forceinline__ void store(uint32_t dst, int tid) const {
+  // Writes fp16 rows; those from `keys` on as zeros.
+  __device__ __forceinline__ void store(uint32_t dst, int tid, int keys) const {
 #pragma unroll
     for (int g = 0; g < 4; ++g)
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const int idx = i * 128 + tid, r32 = idx / UPR, u = idx - r32 * UPR, row = 32 * g + r32;
-        const uint4 v = c[g][i];
+        const uint4 v = row < keys ? c[g][i] : make_uint4(0u, 0u, 0u, 0u);
         const uint32_t line = dst + (u >> 2) * (kChN * 128) + row * 128;
-        const uint32_t a[2][4] = {{e4m3x2_f16x2(v.x), e4m3x2_f16x2(v.x >> 16), e4m3x2_f16x2(v.y), e4m3x2_f16x2(v.y >> 16)},
-                                  {e4m3x2_f16x2(v.z), e4m3x2_f16x2(v.z >> 16), e4m3x2_f16x2(v.w), e4m3x2_f16x2(v.w >> 16)}};
-        // units of the even and odd column blocks go out in opposite order, so
-        // that eight lanes of a row hit all eight 16-byte banks
+        // the units of odd column blocks go out in the opposite order, so that
+        // eight lanes of a row hit all eight 16-byte banks
         const bool odd = (u >> 2) & 1;
-        const int u0 = 2 * (u & 3) + (odd ? 1 : 0), u1 = u0 ^ 1;
-        st_shared_v4(line + ((u0 ^ (row & 7)) << 4), odd ? a[1][0] : a[0][0], odd ? a[1][1] : a[0][1],
-                     odd ? a[1][2] : a[0][2], odd ? a[1][3] : a[0][3]);
-        st_shared_v4(line + ((u1 ^ (row & 7)) << 4), odd ? a[0][0] : a[1][0], odd ? a[0][1] : a[1][1],
-                     odd ? a[0][2] : a[1][2], odd ? a[0][3] : a[1][3]);
+        const uint32_t x0 = odd ? v.z : v.x, x1 = odd ? v.w : v.y, y0 = odd ? v.x : v.z, y1 = odd ? v.y : v.w;
+        const int u0 = 2 * (u & 3) + (odd ? 1 : 0);
+        st_shared_v4(line + ((u0 ^ (row & 7)) << 4), e4m3x2_f16x2(x0), e4m3x2_f16x2(x0 >> 16), e4m3x2_f16x2(x1),
+                     e4m3x2_f16x2(x1 >> 16));
+        st_shared_v4(line + (((u0 ^ 1) ^ (row & 7)) << 4), e4m3x2_f16x2(y0), e4m3x2_f16x2(y0 >> 16), e4m3x2_f16x2(y1),
+                     e4m3x2_f16x2(y1 >> 16));
       }
   }
 };
@@ -301,12 +316,13 @@ struct ChRegs {
 template <int DQK, int DV, bool FP8>
 __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                       const __grid_constant__ CUtensorMap tmV, const PagedAttn p, const ChCodes codes) {
+                       const __grid_constant__ CUtensorMap tmV, const PagedAttn p) {
   using C = ChCfg<DQK, DV, FP8>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* gen = smem_raw + (base - raw);
-  const uint32_t sQ = base, sK = sQ + 2 * C::Q_BYTES, sV = sK + C::SK * C::K_BYTES, sBar = sV + C::SV * C::V_BYTES;
+  const uint32_t sQ = base, sK = sQ + 2 * C::Q_BYTES, sV = sK + C::SK * C::K_BYTES;
+  const uint32_t sKc = sV + C::SV * C::V_BYTES, sVc = sKc + C::KC_BYTES, sBar = sVc + C::VC_BYTES;
   uint8_t* bar_gen = gen + (sBar - base);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_gen + 8 * C::BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bar_gen + 8 * C::BARS + 4);
@@ -318,7 +334,9 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
   const uint32_t bVFull = bKEmpty + 8 * C::SK;   // [SV]
   const uint32_t bVEmpty = bVFull + 8 * C::SV;   // [SV]
   const uint32_t bVTail = bVEmpty + 8 * C::SV;   // a V block whose last rows must be cleared
-  const uint32_t bSFull = bVTail + 8;            // [2]
+  const uint32_t bCFull = bVTail + 8;            // [2] staged codes of K, of V (e4m3)
+  const uint32_t bCEmpty = bCFull + 16;          // [2] in the converters' registers
+  const uint32_t bSFull = bCEmpty + 16;          // [2]
   const uint32_t bSFree = bSFull + 16;           // [1] the S buffer has been copied out
   const uint32_t bPFull = bSFree + 8;            // [2]
   const uint32_t bPDone = bPFull + 16;           // [2]
@@ -341,6 +359,8 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
         mbar_init(bOFull + 8 * t, 1);
         mbar_init(bOEmpty + 8 * t, 128);
         mbar_init(bDrain + 8 * t, 1);
+        mbar_init(bCFull + 8 * t, 1);
+        mbar_init(bCEmpty + 8 * t, 128);
       }
       mbar_init(bSFree, 128);
       mbar_init(bVTail, 1);
@@ -354,11 +374,9 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
       }
       *abort_flag = 0;
       fence_mbar_init();
-      if constexpr (!FP8) {
-        prefetch_tmap(&tmQ);
-        prefetch_tmap(&tmK);
-        prefetch_tmap(&tmV);
-      }
+      if constexpr (!FP8) prefetch_tmap(&tmQ);
+      prefetch_tmap(&tmK);
+      prefetch_tmap(&tmV);
     }
     __syncwarp();
     tmem_alloc(smem_addr(tmem_slot), 512);
@@ -375,28 +393,31 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
   if (warp < 4) {
     setmaxnreg_dec<C::REGS_CTRL>();
     if (warp == 0 || warp == 3) {
-      // ---------------------------------------------------------- copies (bf16 caches)
-      if constexpr (!FP8) {
+      // ---------------------------------------------------------- copies: warp 0 Q and K, warp 3 V
+      {
         const bool is_k = warp == 0;
-        const int nslot = is_k ? C::SK : C::SV;
-        const uint32_t ring = is_k ? sK : sV, slot_bytes = is_k ? C::K_BYTES : C::V_BYTES;
-        const uint32_t bFull = is_k ? bKFull : bVFull, bEmpty = is_k ? bKEmpty : bVEmpty;
+        const int nslot = FP8 ? 1 : (is_k ? C::SK : C::SV);
+        const uint32_t ring = FP8 ? (is_k ? sKc : sVc) : (is_k ? sK : sV);
+        const uint32_t slot_bytes = FP8 ? (is_k ? C::KC_BYTES : C::VC_BYTES) : (is_k ? C::K_BYTES : C::V_BYTES);
+        const uint32_t bFull = FP8 ? (is_k ? bCFull : bCFull + 8) : (is_k ? bKFull : bVFull);
+        const uint32_t bEmpty = FP8 ? (is_k ? bCEmpty : bCEmpty + 8) : (is_k ? bKEmpty : bVEmpty);
         const CUtensorMap* tm = is_k ? &tmK : &tmV;
-        const int chunks = is_k ? C::QK_CHUNKS : C::V_CHUNKS;
+        // one copy takes `box` rows of a page: 128 bytes of them (bf16), or whole rows of codes
+        const int chunks = FP8 ? 1 : (is_k ? C::QK_CHUNKS : C::V_CHUNKS);
+        const uint32_t row_bytes = FP8 ? (is_k ? DQK : DV) : 128;
         const int boxes = kChN / p.box, issues = boxes * chunks, ahead = 32 / boxes;
         const int box = lane / chunks, c = lane - box * chunks;
-        const uint32_t q_bytes = C::QK_CHUNKS * 128 * tpt * p.G;
         uint32_t it = 0, tails = 0, nq[2] = {0, 0};
         bool ok = true;
         for (ChWalk w(p, d, tpt); ok && w.valid(); w.next()) {
-          if (is_k) {
+          if (!FP8 && is_k) {
             for (int t = 0; t < 2 && ok; ++t) {
               if (!w.has(t)) continue;
               if (nq[t] > 0) ok = __all_sync(0xffffffffu, paged_wait(bQEmpty + 8 * t, (nq[t] - 1) & 1, abort_flag));
               if (!ok) break;
               ++nq[t];
               if (lane == 0) {
-                mbar_arrive_expect_tx(bQFull + 8 * t, q_bytes);
+                mbar_arrive_expect_tx(bQFull + 8 * t, C::QK_CHUNKS * 128 * tpt * p.G);
                 for (int i = 0; i < C::QK_CHUNKS; ++i)
                   tma_load_3d(sQ + t * C::Q_BYTES + i * C::CHUNK, &tmQ, bQFull + 8 * t, i * 64, w.h * p.G,
                               w.r.t0 + (2 * w.pair + t) * tpt);
@@ -411,13 +432,13 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
             if (it >= static_cast<uint32_t>(nslot))
               ok = __all_sync(0xffffffffu, paged_wait(bEmpty + 8 * s, ((it / nslot) - 1) & 1, abort_flag));
             if (!ok) break;
-            const bool tail = !is_k && (j + 1) * kChN > w.r.kv;
+            const bool tail = !FP8 && !is_k && (j + 1) * kChN > w.r.kv;
             const uint32_t bar = tail ? bVTail : bFull + 8 * s;
             if (lane == 0) mbar_arrive_expect_tx(bar, slot_bytes);
             __syncwarp();
             const int pg = __shfl_sync(0xffffffffu, page, a * boxes + (lane < issues ? box : 0));
             if (lane < issues)
-              tma_load_4d(ring + s * slot_bytes + c * C::CHUNK + box * p.box * 128, tm, bar, c * 64, w.h,
+              tma_load_4d(ring + s * slot_bytes + c * C::CHUNK + box * p.box * row_bytes, tm, bar, c * 64, w.h,
                           (j * kChN + box * p.box) % p.page_size, pg);
             if (tail) {
               ok = __all_sync(0xffffffffu, paged_wait(bVTail, tails & 1, abort_flag));
@@ -510,18 +531,20 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
     const int r = threadIdx.x - 128 - 128 * t;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t tS = tmem + lanes, tO = tmem + lanes + C::TM_O + 128 * t, tP = tmem + lanes + C::TM_P + 64 * t;
-    const int rtok = r / p.G, rhead = r - rtok * p.G;
+    const uint32_t sWalk = sBar + 512 + 64 * (warp - 4);
     uint32_t g = 0, units = 0;  // key blocks and pieces this tile has done
     bool ok = true;
     for (ChWalk w(p, d, tpt); ok && w.valid(); w.next()) {
+      float c_log2 = p.scale_log2;
+      int see, see_all, end;
+      {
+      const int rtok = r / p.G, rhead = r - rtok * p.G;
       const int tok = (2 * w.pair + t) * tpt + rtok;
       const bool real = rtok < tpt && tok < w.r.nq;
       const bool whole = w.whole(), head = w.kb > 0;
-      const int slot = 2 * blockIdx.x + (head ? 0 : 1);
-      const int64_t part = static_cast<int64_t>(slot) * p.slot_rows + t * tpt * p.G + r;
       if (t == 0 && r == 0 && !whole && !head) {
         PartDesc e;
-        e.last = (w.at + max(w.n0, w.n1) - 1) / d.per;
+        e.last = w.last() / d.per;
         e.t0 = w.r.t0;
         e.row0 = 2 * w.pair * tpt * p.G;
         e.nrows = min(2 * tpt, w.r.nq - 2 * w.pair * tpt) * p.G;
@@ -531,12 +554,13 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
       }
       if (!w.has(t)) {  // none of this tile's blocks are in this piece
         if (real && !whole) {
+          const int64_t part =
+              static_cast<int64_t>(2 * blockIdx.x + (head ? 0 : 1)) * p.slot_rows + t * tpt * p.G + r;
           p.part_ml[2 * part] = -INFINITY;
           p.part_ml[2 * part + 1] = 0.0f;
         }
         continue;
       }
-      float c_log2 = p.scale_log2, v_mult = 1.0f;
       if constexpr (FP8) {
         // this row of Q as fp16, its largest element brought to [1/2, 1)
         constexpr int W = DQK / 2;
@@ -556,7 +580,6 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
         if (amax > 0.0f && amax < INFINITY) e = max(-126, min(126, static_cast<int>(__float_as_uint(amax) >> 23) - 126));
         const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
         c_log2 *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * __ldg(p.k_scale + w.h);
-        v_mult = __ldg(p.v_scale + w.h);
         if (units > 0) ok = paged_wait(bQEmpty + 8 * t, (units - 1) & 1, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -576,12 +599,16 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
       c_log2 = fmaxf(c_log2, 1e-30f);  // a zero scale behaves as a tiny one
       // keys this row sees: j <= see; the tile's first row sees fewest
       const int off = p.causal ? w.r.kv - w.r.nq : w.r.kv - 1;
-      const int see = p.causal ? min(off + tok, w.r.kv - 1) : off;
-      const int see_all = p.causal ? min(off + (2 * w.pair + t) * tpt, w.r.kv - 1) : off;
+      see = p.causal ? min(off + tok, w.r.kv - 1) : off;
+      see_all = p.causal ? min(off + (2 * w.pair + t) * tpt, w.r.kv - 1) : off;
+
+      end = w.end(t);
+      w.put(sWalk);
+      }
 
       float m_run = -INFINITY, l_run = 0.0f;
-      const int end = w.end(t);
-      for (int j = w.kb; j < end; ++j, ++g) {
+      const int kb = w.kb;
+      for (int j = kb; j < end; ++j, ++g) {
         ok = __all_sync(0xffffffffu, paged_wait(bSFull + 8 * t, g & 1, abort_flag));
         if (!ok) break;
         tc_fence_after();
@@ -652,7 +679,7 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
 
         // P and O are free once PV of the tile's block before has completed
         bool w_ok = g == 0 || paged_wait(bPDone + 8 * t, (g - 1) & 1, abort_flag);
-        const bool resc = j > w.kb && __any_sync(0xffffffffu, need);
+        const bool resc = j > kb && __any_sync(0xffffffffu, need);
         ok = __all_sync(0xffffffffu, w_ok);
         if (!ok) break;
         tc_fence_after();
@@ -678,6 +705,14 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
       ok = __all_sync(0xffffffffu, paged_wait(bOFull + 8 * t, (units - 1) & 1, abort_flag));
       if (!ok) break;
       tc_fence_after();
+      w.get(sWalk);
+      const int rtok = r / p.G, rhead = r - rtok * p.G;
+      const int tok = (2 * w.pair + t) * tpt + rtok;
+      const bool real = rtok < tpt && tok < w.r.nq;
+      const bool whole = w.whole();
+      const int64_t part =
+          static_cast<int64_t>(2 * blockIdx.x + (w.kb > 0 ? 0 : 1)) * p.slot_rows + t * tpt * p.G + r;
+      const float v_mult = FP8 ? __ldg(p.v_scale + w.h) : 1.0f;
       const float inv = !whole ? 1.0f : (l_run == 0.0f ? 0.0f : v_mult / l_run);
       const int hq = w.h * p.G + rhead;
       __nv_bfloat16* orow = p.o + (static_cast<int64_t>(w.r.t0 + (real ? tok : 0)) * p.Hq + (real ? hq : 0)) * DV;
@@ -719,41 +754,35 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
     if constexpr (FP8) {
       setmaxnreg_dec<C::REGS_CONV>();
       const int tid = threadIdx.x - 384;
-      ChRegs<DQK> kr;
-      ChRegs<DV> vr;
+      const uint4* kc = reinterpret_cast<const uint4*>(gen + (sKc - base));
+      const uint4* vc = reinterpret_cast<const uint4*>(gen + (sVc - base));
       uint32_t it = 0;
       bool ok = true;
-      // lane i holds the page of 16-key group i of the block to load
-      ChWalk nx(p, d, tpt);  // runs one block ahead
-      int nj = nx.kb;
-      auto pages_of = [&]() { return lane < 8 ? paged_page(p, nx.b, nj * kChN + 16 * lane, nx.r.kv) : 0; };
-      int pages = 0;
-      bool more = nx.valid();
-      if (more) {
-        pages = pages_of();
-        kr.load(codes, 0, nx.h, nj * kChN, nx.r.kv, pages, p.page_size, p.num_pages, tid);
-        vr.load(codes, 1, nx.h, nj * kChN, nx.r.kv, pages, p.page_size, p.num_pages, tid);
-      }
-      for (; more && ok; ++it) {
-        const uint32_t ks = it % C::SK, vs = it % C::SV;
-        if (++nj >= nx.ke) {
-          nx.next();
-          nj = nx.kb;
-          more = nx.valid();
+      // staged codes -> registers -> fp16 tile, once the tile's last products are done
+      auto turn = [&](auto& regs, const uint4* staged, int which, uint32_t bFull, uint32_t bEmpty, uint32_t dst, int n,
+                      int keys, uint32_t bytes) {
+        const uint32_t s = it % n;
+        ok = __all_sync(0xffffffffu, paged_wait(bCFull + 8 * which, it & 1, abort_flag));
+        if (!ok) return;
+        regs.load(staged, tid);
+        mbar_arrive(bCEmpty + 8 * which);
+        if (it >= static_cast<uint32_t>(n))
+          ok = __all_sync(0xffffffffu, paged_wait(bEmpty + 8 * s, ((it / n) - 1) & 1, abort_flag));
+        if (!ok) return;
+        regs.store(dst + s * bytes, tid, keys);
+        fence_proxy_async_smem();
+        mbar_arrive(bFull + 8 * s);
+      };
+      for (ChWalk w(p, d, tpt); ok && w.valid(); w.next()) {
+        for (int j = w.kb; j < w.ke && ok; ++j, ++it) {
+          {
+            ChRegs<DQK> kr;
+            turn(kr, kc, 0, bKFull, bKEmpty, sK, C::SK, kChN, C::K_BYTES);  // masked scores need no clean keys
+          }
+          if (!ok) break;
+          ChRegs<DV> vr;
+          turn(vr, vc, 1, bVFull, bVEmpty, sV, C::SV, w.r.kv - j * kChN, C::V_BYTES);
         }
-        if (more) pages = pages_of();
-        if (it >= C::SK) ok = __all_sync(0xffffffffu, paged_wait(bKEmpty + 8 * ks, ((it / C::SK) - 1) & 1, abort_flag));
-        if (!ok) break;
-        kr.store(sK + ks * C::K_BYTES, tid);
-        fence_proxy_async_smem();
-        mbar_arrive(bKFull + 8 * ks);
-        if (more) kr.load(codes, 0, nx.h, nj * kChN, nx.r.kv, pages, p.page_size, p.num_pages, tid);
-        if (it >= C::SV) ok = __all_sync(0xffffffffu, paged_wait(bVEmpty + 8 * vs, ((it / C::SV) - 1) & 1, abort_flag));
-        if (!ok) break;
-        vr.store(sV + vs * C::V_BYTES, tid);
-        fence_proxy_async_smem();
-        mbar_arrive(bVFull + 8 * vs);
-        if (more) vr.load(codes, 1, nx.h, nj * kChN, nx.r.kv, pages, p.page_size, p.num_pages, tid);
       }
     }
   }

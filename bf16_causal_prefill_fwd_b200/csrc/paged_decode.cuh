@@ -522,11 +522,15 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<DQK, DV, FP8, NT>::BLOCKS)
 
 // Joins the parts of the units that several blocks have worked on: block c of
 // the grid takes the unit that begins, but does not end, in block c; its rows
-// are spread over gridDim.y. O = sum_b 2^(m_b - M) O_b / sum_b 2^(m_b - M) l_b.
-// A row may have hundreds of parts (one long request over the whole GPU), so
-// its parts are read side by side: lane i of every warp has (m, l) of part i,
-// the four warps add every fourth part's O (16 bytes per lane, several loads in
-// flight), and their sums meet in shared memory. The order is fixed.
+// are spread over gridDim.y. O = sum_b 2^(m_b - M) O_b / sum_b 2^(m_b - M) l_b,
+// added in block order. Lane i of a warp has (m, l) of part i, and the warp reads
+// O of one part after the other, 16 bytes per lane, several loads in flight.
+// With few parts a warp takes a row by itself; a row may also have hundreds (one
+// long request over the whole GPU), and then the four warps add every fourth
+// part each and meet in shared memory. 16 is where the second way's two barriers
+// cost less than a warp's longer chain of loads.
+constexpr int kJoinAlone = 16;
+
 template <int DV>
 __global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttn p) {
   static_assert(DV == 128, "a warp reads a row of O with 16 bytes per lane");
@@ -536,14 +540,17 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttn p) {
   const PartDesc e = reinterpret_cast<const PartDesc*>(p.desc)[c];
   if (e.last < 0) return;
   const int parts = e.last - c + 1;
-  // part i: the tail slot of the first block, then the head slots of the next ones
-  auto slot_row = [&](int i, int r) {
-    return static_cast<int64_t>(2 * (c + i) + (i == 0 ? 1 : 0)) * p.slot_rows + r;
-  };
-  for (int r = blockIdx.y; r < e.nrows; r += gridDim.y) {
+  const bool alone = parts <= kJoinAlone;
+  const int first = alone ? 0 : warp, step = alone ? 1 : 4;  // this warp's parts of its row
+  const float v_scale = p.v_scale != nullptr ? __ldg(p.v_scale + e.hkv) : 1.0f;
+  for (int r = alone ? 4 * blockIdx.y + warp : blockIdx.y; r < e.nrows; r += alone ? 4 * gridDim.y : gridDim.y) {
+    // part i: the tail slot of the first block, then the head slots of the next ones
+    const float* ml = p.part_ml + 2 * static_cast<int64_t>(r);
+    const float* po = p.part_o + static_cast<int64_t>(r) * DV + 4 * lane;
+    auto slot = [&](int i) { return static_cast<int64_t>(2 * (c + i) + (i == 0 ? 1 : 0)) * p.slot_rows; };
     float mm = -INFINITY;
     for (int i = lane; i < parts; i += 32) {
-      const float2 x = *reinterpret_cast<const float2*>(p.part_ml + 2 * slot_row(i, r));
+      const float2 x = *reinterpret_cast<const float2*>(ml + 2 * slot(i));
       if (x.y != 0.0f) mm = fmaxf(mm, x.x);  // a part with l = 0 saw none of the row's keys
     }
 #pragma unroll
@@ -553,7 +560,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttn p) {
     for (int i0 = 0; i0 < parts; i0 += 32) {
       float f = 0.0f;
       if (i0 + lane < parts) {
-        const float2 x = *reinterpret_cast<const float2*>(p.part_ml + 2 * slot_row(i0 + lane, r));
+        const float2 x = *reinterpret_cast<const float2*>(ml + 2 * slot(i0 + lane));
         if (x.y != 0.0f) {
           f = ex2_approx(x.x - mm);
           ll = fmaf(x.y, f, ll);
@@ -561,9 +568,9 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttn p) {
       }
       const int n = min(32, parts - i0);
 #pragma unroll 4
-      for (int i = warp; i < n; i += 4) {
+      for (int i = first; i < n; i += step) {
         const float w = __shfl_sync(0xffffffffu, f, i);
-        const float4 o = *reinterpret_cast<const float4*>(p.part_o + slot_row(i0 + i, r) * DV + 4 * lane);
+        const float4 o = *reinterpret_cast<const float4*>(po + slot(i0 + i) * DV);
         if (w != 0.0f) {  // a part without keys may have left O unwritten
           acc.x = fmaf(o.x, w, acc.x);
           acc.y = fmaf(o.y, w, acc.y);
@@ -574,16 +581,21 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttn p) {
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, o);
-    *reinterpret_cast<float4*>(&s_o[warp][4 * lane]) = acc;
-    __syncthreads();
     const int row = e.row0 + r, tok = row / p.G, hq = e.hkv * p.G + row - tok * p.G;
-    const int td = threadIdx.x;
-    const float sum = (s_o[0][td] + s_o[1][td]) + (s_o[2][td] + s_o[3][td]);
-    const float inv = ll == 0.0f ? 0.0f : (p.v_scale != nullptr ? __ldg(p.v_scale + e.hkv) : 1.0f) / ll;
-    p.o[(static_cast<int64_t>(e.t0 + tok) * p.Hq + hq) * DV + td] = __float2bfloat16(sum * inv);
-    if (p.lse != nullptr && td == 0)
+    const float inv = ll == 0.0f ? 0.0f : v_scale / ll;
+    __nv_bfloat16* out = p.o + (static_cast<int64_t>(e.t0 + tok) * p.Hq + hq) * DV;
+    if (alone) {
+      *reinterpret_cast<uint2*>(out + 4 * lane) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    } else {
+      *reinterpret_cast<float4*>(&s_o[warp][4 * lane]) = acc;
+      __syncthreads();
+      const int td = threadIdx.x;
+      out[td] = __float2bfloat16(((s_o[0][td] + s_o[1][td]) + (s_o[2][td] + s_o[3][td])) * inv);
+      __syncthreads();  // s_o is written again
+    }
+    if (p.lse != nullptr && lane == 0 && (alone || warp == 0))
       p.lse[static_cast<int64_t>(hq) * p.T + e.t0 + tok] = ll == 0.0f ? -INFINITY : (mm + fast_log2(ll)) * kLn2;
-    __syncthreads();  // s_o is written again
   }
 }
 
