@@ -113,8 +113,8 @@ int check_cache(const b200attn_paged_cache* c) {
 }
 
 // A cache tensor as a 4-D map {d, head, row of the page, page} with a box of one
-// head of `rows` rows: 128 bytes of each with the 128-byte swizzle, or (swizzle
-// false) whole rows as they are; out of range reads zero.
+// head of `rows` rows, 128 bytes of each, with the 128-byte swizzle or (swizzle
+// false) as they are; out of range reads zero.
 bool page_map(CUtensorMap* m, const void* ptr, bool fp8, int d, int H, int ps, int pages, int64_t head, int64_t token,
               int64_t page, int rows, bool swizzle) {
   EncodeTiledFn enc = encode_fn();
@@ -125,20 +125,24 @@ bool page_map(CUtensorMap* m, const void* ptr, bool fp8, int d, int H, int ps, i
                    sp = pages > 1 ? page * esz : d * esz;
   const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)ps, (cuuint64_t)pages};
   const cuuint64_t strides[3] = {sh, st, sp};
-  const cuuint32_t box[4] = {swizzle ? (cuuint32_t)(128 / esz) : (cuuint32_t)d, 1, (cuuint32_t)rows, 1};
+  const cuuint32_t box[4] = {(cuuint32_t)(128 / esz), 1, (cuuint32_t)rows, 1};
   const cuuint32_t one[4] = {1, 1, 1, 1};
   return enc(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr),
              dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
              swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             // no more than a row: the bytes behind it are another head's (256 bytes at a time read 1.4 times
+             // an e4m3 cache's 128-byte rows from HBM)
+             fp8 ? (d % 128 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B)
+                 : (d % 128 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B),
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool page_maps(CUtensorMap* tk, CUtensorMap* tv, const b200attn_paged_cache* c, int rows, bool swizzle) {
+bool page_maps(CUtensorMap* tk, CUtensorMap* tv, const b200attn_paged_cache* c, int rows, bool swizzle_v) {
   const bool fp8 = c->dtype == B200ATTN_FP8_E4M3;
   return page_map(tk, c->k, fp8, c->d_qk, c->Hkv, c->page_size, c->num_pages, c->k_head_stride, c->k_token_stride,
-                  c->k_page_stride, rows, swizzle) &&
+                  c->k_page_stride, rows, true) &&
          page_map(tv, c->v, fp8, c->d_v, c->Hkv, c->page_size, c->num_pages, c->v_head_stride, c->v_token_stride,
-                  c->v_page_stride, rows, swizzle);
+                  c->v_page_stride, rows, swizzle_v);
 }
 
 // Launch whose blocks may be scheduled while the kernel before it drains (that

@@ -20,16 +20,22 @@
 // joined in block order by paged_join_kernel. Every block finds its run from
 // the lengths in device memory.
 //
-// Keys and values. bf16: one warp copies K, one V, page piece by page piece
-// (TMA, 128-byte swizzle; pages behind the last are read as zeros through an
+// Keys and values. One warp copies K, one V, page piece by page piece (TMA,
+// 128-byte swizzle; pages behind the last are read as zeros through an
 // out-of-range page number). The rows behind the last key inside its page may
 // hold anything, and 0 * NaN is NaN, so the V warp clears them in shared memory
-// before the tensor core reads them; scores are replaced by select. e4m3: the same
-// warps copy the codes of a block to a staging tile, and four more warps turn
-// them into fp16 exactly and write the swizzled tiles (about 20 instructions
-// per 16 codes, beside the softmax's eight warps); the staging tile is free for
-// the next block as soon as they hold it in registers. Q becomes fp16 too, after
-// a power of two per row.
+// before the tensor core reads them; scores are replaced by select.
+//
+// e4m3 caches. S = Q K^T stays in e4m3 on the K side without losing Q: after a
+// power of two per row (its largest element in [2^7, 2^8)), a bf16 number is the
+// sum of two e4m3 numbers -- the one nearest to it (4 bits) and the rest (4
+// bits) -- exactly for elements within 2^-10 of the row's largest, to 2^-18 of it
+// below. Both halves are products of kind::f8f6f4 into one accumulator, at twice
+// the rate of 16 bits each, so K's codes go to the tensor core as they are. P
+// would need the same split in the softmax, the busiest warps here; instead V's
+// codes become fp16 (exactly) in shared memory, by the two copying warps, and P
+// is fp16. Converting K as well, with four more warps, took 503 us where this
+// takes 390 (4 requests of 500-1300 new tokens, 2-12k keys).
 //
 // Bound by the tensor core (2 x 2 x 128^3 products per key block and pair) and,
 // for chunks of a few tokens, by reading the cache.
@@ -44,35 +50,37 @@ constexpr int kChN = 128;  // keys per block
 constexpr int kChRows = 2 * kChM;
 // What a unit costs beyond its key blocks (its Q, the pipeline's filling, its
 // output), in key blocks: counted in when the line is cut, so that a run of many
-// short units is not longer than one of few long ones.
-constexpr int kChUnitCost = 2;
+// short units is not longer than one of few long ones. Measured on ragged chunks
+// of 1-1500 tokens and on one 2048-token prompt: 1 block 228 and 88 us, 2 210 and
+// 81, 3 200 and 74, 4 200 and 75, 6 195 and 77.
+constexpr int kChUnitCost = 3;
 constexpr int kChMaxBlocks = 160;  // workspace slots are sized for this many blocks
 
 template <int DQK, int DV, bool FP8>
 struct ChCfg {
-  static constexpr int THREADS = FP8 ? 512 : 384;
-  static constexpr int REGS_LAUNCH = FP8 ? 128 : 168;
-  // Register split by warpgroup: control, converters (e4m3), softmax. The sums
-  // stay within what the block was launched with.
-  static constexpr int REGS_CTRL = 72;
-  static constexpr int REGS_CONV = 88;
-  static constexpr int REGS_SOFT = FP8 ? 176 : 208;
-  static_assert(128 * REGS_CTRL + (FP8 ? 128 * REGS_CONV : 0) + 256 * REGS_SOFT <= THREADS * REGS_LAUNCH, "registers");
+  static constexpr int THREADS = 384, REGS_LAUNCH = 168;
+  // Register split by warpgroup: copies and issue, softmax; the sum stays within
+  // what the block was launched with.
+  static constexpr int REGS_CTRL = FP8 ? 80 : 72, REGS_SOFT = FP8 ? 200 : 208;
+  static_assert(128 * REGS_CTRL + 256 * REGS_SOFT <= THREADS * REGS_LAUNCH, "registers");
   static constexpr int CHUNK = kChM * 128;  // 128 rows x 128 bytes, swizzled
-  static constexpr int QK_CHUNKS = DQK / 64, V_CHUNKS = DV / 64;
-  static constexpr int Q_BYTES = QK_CHUNKS * CHUNK, K_BYTES = QK_CHUNKS * CHUNK, V_BYTES = V_CHUNKS * CHUNK;
-  static constexpr int KC_BYTES = FP8 ? kChN * DQK : 0, VC_BYTES = FP8 ? kChN * DV : 0;  // staged codes
-  static constexpr int AVAIL = 227 * 1024 - 2048 - 2 * Q_BYTES - KC_BYTES - VC_BYTES;
+  static constexpr int KSZ = FP8 ? 1 : 2;
+  static constexpr int Q_CHUNKS = 2 * DQK / 128;  // bf16, or two halves of codes side by side
+  static constexpr int K_CHUNKS = (DQK * KSZ + 127) / 128, V_CHUNKS = DV / 64;
+  static constexpr int Q_BYTES = Q_CHUNKS * CHUNK, K_BYTES = K_CHUNKS * CHUNK, V_BYTES = V_CHUNKS * CHUNK;
+  static constexpr int STAGES = FP8 ? 2 : 0, VC_BYTES = kChN * DV;  // staged codes of V
+  static constexpr int AVAIL = 227 * 1024 - 2048 - 2 * Q_BYTES - STAGES * VC_BYTES;
   static constexpr int PAIRS = AVAIL / (K_BYTES + V_BYTES);
   static constexpr int SV = PAIRS >= 2 ? 2 : 1;
-  static constexpr int SK = (AVAIL - SV * V_BYTES) / K_BYTES > 3 ? 3 : (AVAIL - SV * V_BYTES) / K_BYTES;
+  static constexpr int SK_FIT = (AVAIL - SV * V_BYTES) / K_BYTES, SK = SK_FIT > 4 ? 4 : SK_FIT;
   static constexpr int BARS = 2 + 2 + 2 * SK + 2 * SV + 1 + 4 + 2 + 1 + 2 + 2 + 2 + 2 + 2;
-  static constexpr int SMEM = 2 * Q_BYTES + SK * K_BYTES + SV * V_BYTES + KC_BYTES + VC_BYTES + 1024 + 1024;
-  static_assert(8 * BARS + 8 <= 512 && 512 + 8 * 64 <= 1024 && SMEM <= 227 * 1024 && SK >= 1, "shared memory");
+  static constexpr int SMEM = 2 * Q_BYTES + SK * K_BYTES + SV * V_BYTES + STAGES * VC_BYTES + 1024 + 1024;
+  static_assert(8 * BARS + 8 <= 512 && 512 + 8 * 64 <= 1024 && SMEM <= 227 * 1024 && SK >= 2, "shared memory");
   // Tensor memory: S [0, 128) for both tiles in turn, O_t at 128 + 128 t, P_t
   // (16-bit, 64 columns) at 384 + 64 t.
   static constexpr int TM_O = 128, TM_P = 384;
-  // Operand format of kind::f16: 1 = bf16, 0 = fp16.
+  // Instruction descriptors: kind::f16 with bf16 (format 1), or kind::f8f6f4 with
+  // e4m3 (0) for S and kind::f16 with fp16 (0) for O.
   static constexpr uint32_t FMT = FP8 ? 0u : 1u;
   static constexpr uint32_t IDESC_QK = idesc_dense(FMT, FMT, kChM, kChN, false);
   static constexpr uint32_t IDESC_PV = idesc_dense(FMT, FMT, kChM, DV, true);
@@ -264,6 +272,12 @@ __device__ __forceinline__ void ch_exp2_fma(float x0, float x1, float& r0, float
   r1 = x1 >= -125.0f ? __uint_as_float(__float_as_uint(p1) + (__float_as_uint(j1) << 23)) : 0.0f;
 }
 
+__device__ __forceinline__ __half2 bits_half2(uint32_t x) {
+  __half2 h;
+  memcpy(&h, &x, 4);
+  return h;
+}
+
 // Largest of three; NaN if one of them is.
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float r;
@@ -279,39 +293,31 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, 
       : "memory");
 }
 
-// One staged block of 128 keys of K or V: thread `tid` of 128 takes, of each 32
-// keys, units tid, tid + 128, ... (16 codes each, D / 16 to a row).
-template <int D>
-struct ChRegs {
-  static constexpr int UPR = D / 16, PER = 32 * UPR / 128;
-  uint4 c[4][PER];
-  __device__ __forceinline__ void load(const uint4* staged, int tid) {
+// Rows [64 half, 64 half + 64) of a staged 128 x 128 block of V's codes -> the
+// fp16 tile, by one warp; rows from `keys` on as zeros.
+__device__ __forceinline__ void ch_convert_v(const uint4* staged, uint32_t dst, int half, int lane, int keys) {
+  const int u = lane & 7;           // 16 codes of a row: columns 16 u ..
+  const bool odd = (u >> 2) & 1;    // second column block: its units go out in the opposite order,
+  const int u0 = 2 * (u & 3) + (odd ? 1 : 0);  // so that eight lanes of a row hit all eight 16-byte banks
+  const uint32_t col = dst + (u >> 2) * (kChN * 128);
+#pragma unroll 1
+  for (int g = 0; g < 4; ++g) {
+    uint4 c[4];
 #pragma unroll
-    for (int g = 0; g < 4; ++g)
+    for (int i = 0; i < 4; ++i) c[i] = staged[(64 * half + 16 * g) * 8 + 32 * i + lane];
 #pragma unroll
-      for (int i = 0; i < PER; ++i) c[g][i] = staged[g * 32 * UPR + i * 128 + tid];
+    for (int i = 0; i < 4; ++i) {
+      const int row = 64 * half + 16 * g + 4 * i + (lane >> 3);
+      const uint4 v = row < keys ? c[i] : make_uint4(0u, 0u, 0u, 0u);
+      const uint32_t line = col + row * 128;
+      const uint32_t x0 = odd ? v.z : v.x, x1 = odd ? v.w : v.y, y0 = odd ? v.x : v.z, y1 = odd ? v.y : v.w;
+      st_shared_v4(line + ((u0 ^ (row & 7)) << 4), e4m3x2_f16x2(x0), e4m3x2_f16x2(x0 >> 16), e4m3x2_f16x2(x1),
+                   e4m3x2_f16x2(x1 >> 16));
+      st_shared_v4(line + (((u0 ^ 1) ^ (row & 7)) << 4), e4m3x2_f16x2(y0), e4m3x2_f16x2(y0 >> 16), e4m3x2_f16x2(y1),
+                   e4m3x2_f16x2(y1 >> 16));
+    }
   }
-  // Writes fp16 rows; those from `keys` on as zeros.
-  __device__ __forceinline__ void store(uint32_t dst, int tid, int keys) const {
-#pragma unroll
-    for (int g = 0; g < 4; ++g)
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int idx = i * 128 + tid, r32 = idx / UPR, u = idx - r32 * UPR, row = 32 * g + r32;
-        const uint4 v = row < keys ? c[g][i] : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t line = dst + (u >> 2) * (kChN * 128) + row * 128;
-        // the units of odd column blocks go out in the opposite order, so that
-        // eight lanes of a row hit all eight 16-byte banks
-        const bool odd = (u >> 2) & 1;
-        const uint32_t x0 = odd ? v.z : v.x, x1 = odd ? v.w : v.y, y0 = odd ? v.x : v.z, y1 = odd ? v.y : v.w;
-        const int u0 = 2 * (u & 3) + (odd ? 1 : 0);
-        st_shared_v4(line + ((u0 ^ (row & 7)) << 4), e4m3x2_f16x2(x0), e4m3x2_f16x2(x0 >> 16), e4m3x2_f16x2(x1),
-                     e4m3x2_f16x2(x1 >> 16));
-        st_shared_v4(line + (((u0 ^ 1) ^ (row & 7)) << 4), e4m3x2_f16x2(y0), e4m3x2_f16x2(y0 >> 16), e4m3x2_f16x2(y1),
-                     e4m3x2_f16x2(y1 >> 16));
-      }
-  }
-};
+}
 
 template <int DQK, int DV, bool FP8>
 __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
@@ -322,7 +328,7 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
   const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* gen = smem_raw + (base - raw);
   const uint32_t sQ = base, sK = sQ + 2 * C::Q_BYTES, sV = sK + C::SK * C::K_BYTES;
-  const uint32_t sKc = sV + C::SV * C::V_BYTES, sVc = sKc + C::KC_BYTES, sBar = sVc + C::VC_BYTES;
+  const uint32_t sVc = sV + C::SV * C::V_BYTES, sBar = sVc + C::STAGES * C::VC_BYTES;
   uint8_t* bar_gen = gen + (sBar - base);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_gen + 8 * C::BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bar_gen + 8 * C::BARS + 4);
@@ -334,8 +340,8 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
   const uint32_t bVFull = bKEmpty + 8 * C::SK;   // [SV]
   const uint32_t bVEmpty = bVFull + 8 * C::SV;   // [SV]
   const uint32_t bVTail = bVEmpty + 8 * C::SV;   // a V block whose last rows must be cleared
-  const uint32_t bCFull = bVTail + 8;            // [2] staged codes of K, of V (e4m3)
-  const uint32_t bCEmpty = bCFull + 16;          // [2] in the converters' registers
+  const uint32_t bCFull = bVTail + 8;            // [2] staged codes of V (e4m3)
+  const uint32_t bCEmpty = bCFull + 16;          // [2] converted
   const uint32_t bSFull = bCEmpty + 16;          // [2]
   const uint32_t bSFree = bSFull + 16;           // [1] the S buffer has been copied out
   const uint32_t bPFull = bSFree + 8;            // [2]
@@ -360,16 +366,16 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
         mbar_init(bOEmpty + 8 * t, 128);
         mbar_init(bDrain + 8 * t, 1);
         mbar_init(bCFull + 8 * t, 1);
-        mbar_init(bCEmpty + 8 * t, 128);
+        mbar_init(bCEmpty + 8 * t, 64);
       }
       mbar_init(bSFree, 128);
       mbar_init(bVTail, 1);
       for (int s = 0; s < C::SK; ++s) {
-        mbar_init(bKFull + 8 * s, FP8 ? 128 : 1);
+        mbar_init(bKFull + 8 * s, 1);
         mbar_init(bKEmpty + 8 * s, 1);
       }
       for (int s = 0; s < C::SV; ++s) {
-        mbar_init(bVFull + 8 * s, FP8 ? 128 : 1);
+        mbar_init(bVFull + 8 * s, FP8 ? 64 : 1);
         mbar_init(bVEmpty + 8 * s, 1);
       }
       *abort_flag = 0;
@@ -394,52 +400,55 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
     setmaxnreg_dec<C::REGS_CTRL>();
     if (warp == 0 || warp == 3) {
       // ---------------------------------------------------------- copies: warp 0 Q and K, warp 3 V
-      {
-        const bool is_k = warp == 0;
-        const int nslot = FP8 ? 1 : (is_k ? C::SK : C::SV);
-        const uint32_t ring = FP8 ? (is_k ? sKc : sVc) : (is_k ? sK : sV);
-        const uint32_t slot_bytes = FP8 ? (is_k ? C::KC_BYTES : C::VC_BYTES) : (is_k ? C::K_BYTES : C::V_BYTES);
-        const uint32_t bFull = FP8 ? (is_k ? bCFull : bCFull + 8) : (is_k ? bKFull : bVFull);
-        const uint32_t bEmpty = FP8 ? (is_k ? bCEmpty : bCEmpty + 8) : (is_k ? bKEmpty : bVEmpty);
-        const CUtensorMap* tm = is_k ? &tmK : &tmV;
-        // one copy takes `box` rows of a page: 128 bytes of them (bf16), or whole rows of codes
-        const int chunks = FP8 ? 1 : (is_k ? C::QK_CHUNKS : C::V_CHUNKS);
-        const uint32_t row_bytes = FP8 ? (is_k ? DQK : DV) : 128;
-        const int boxes = kChN / p.box, issues = boxes * chunks, ahead = 32 / boxes;
-        const int box = lane / chunks, c = lane - box * chunks;
+      const bool is_k = warp == 0;
+      const bool staged = FP8 && !is_k;
+      const uint32_t nslot = staged ? C::STAGES : (is_k ? C::SK : C::SV);
+      const uint32_t ring = staged ? sVc : (is_k ? sK : sV);
+      const uint32_t slot_bytes = staged ? C::VC_BYTES : (is_k ? C::K_BYTES : C::V_BYTES);
+      const uint32_t bFull = staged ? bCFull : (is_k ? bKFull : bVFull);
+      const uint32_t bEmpty = staged ? bCEmpty : (is_k ? bKEmpty : bVEmpty);
+      const CUtensorMap* tm = is_k ? &tmK : &tmV;
+      // one copy takes `box` rows of a page, 128 bytes of each (staged codes of V: a row)
+      const int chunks = staged ? 1 : (is_k ? C::K_CHUNKS : C::V_CHUNKS);
+      const int boxes = kChN / p.box, issues = boxes * chunks, ahead = 32 / boxes;
+      const int box = lane / chunks, c = lane - box * chunks;
+      int page = 0;
+      bool ok = true;
+      // Block j (the it-th of the ring) of the walk's unit; `bar` counts its bytes.
+      auto copy_block = [&](const ChWalk& w, int j, uint32_t s, uint32_t bar) {
+        const int a = (j - w.kb) % ahead;
+        if (a == 0) page = lane < ahead * boxes ? paged_page(p, w.b, j * kChN + lane * p.box, w.r.kv) : 0;
+        if (lane == 0) mbar_arrive_expect_tx(bar, slot_bytes);
+        __syncwarp();
+        const int pg = __shfl_sync(0xffffffffu, page, a * boxes + (lane < issues ? box : 0));
+        if (lane < issues)
+          tma_load_4d(ring + s * slot_bytes + c * C::CHUNK + box * p.box * 128, tm, bar, c * (128 / C::KSZ), w.h,
+                      (j * kChN + box * p.box) % p.page_size, pg);
+      };
+      if constexpr (!FP8) {
         uint32_t it = 0, tails = 0, nq[2] = {0, 0};
-        bool ok = true;
         for (ChWalk w(p, d, tpt); ok && w.valid(); w.next()) {
-          if (!FP8 && is_k) {
+          if (is_k) {
             for (int t = 0; t < 2 && ok; ++t) {
               if (!w.has(t)) continue;
               if (nq[t] > 0) ok = __all_sync(0xffffffffu, paged_wait(bQEmpty + 8 * t, (nq[t] - 1) & 1, abort_flag));
               if (!ok) break;
               ++nq[t];
               if (lane == 0) {
-                mbar_arrive_expect_tx(bQFull + 8 * t, C::QK_CHUNKS * 128 * tpt * p.G);
-                for (int i = 0; i < C::QK_CHUNKS; ++i)
+                mbar_arrive_expect_tx(bQFull + 8 * t, C::Q_CHUNKS * 128 * tpt * p.G);
+                for (int i = 0; i < C::Q_CHUNKS; ++i)
                   tma_load_3d(sQ + t * C::Q_BYTES + i * C::CHUNK, &tmQ, bQFull + 8 * t, i * 64, w.h * p.G,
                               w.r.t0 + (2 * w.pair + t) * tpt);
               }
             }
           }
-          int page = 0;
           for (int j = w.kb; j < w.ke && ok; ++j, ++it) {
-            const int a = (j - w.kb) % ahead;
-            if (a == 0) page = lane < ahead * boxes ? paged_page(p, w.b, j * kChN + lane * p.box, w.r.kv) : 0;
             const uint32_t s = it % nslot;
-            if (it >= static_cast<uint32_t>(nslot))
+            if (it >= nslot)
               ok = __all_sync(0xffffffffu, paged_wait(bEmpty + 8 * s, ((it / nslot) - 1) & 1, abort_flag));
             if (!ok) break;
-            const bool tail = !FP8 && !is_k && (j + 1) * kChN > w.r.kv;
-            const uint32_t bar = tail ? bVTail : bFull + 8 * s;
-            if (lane == 0) mbar_arrive_expect_tx(bar, slot_bytes);
-            __syncwarp();
-            const int pg = __shfl_sync(0xffffffffu, page, a * boxes + (lane < issues ? box : 0));
-            if (lane < issues)
-              tma_load_4d(ring + s * slot_bytes + c * C::CHUNK + box * p.box * row_bytes, tm, bar, c * 64, w.h,
-                          (j * kChN + box * p.box) % p.page_size, pg);
+            const bool tail = !is_k && (j + 1) * kChN > w.r.kv;
+            copy_block(w, j, s, tail ? bVTail : bFull + 8 * s);
             if (tail) {
               ok = __all_sync(0xffffffffu, paged_wait(bVTail, tails & 1, abort_flag));
               ++tails;
@@ -454,8 +463,42 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
             }
           }
         }
-        if (!ok) __nanosleep(200000);  // copies in flight land before the block ends
+      } else {
+        // Each warp keeps its ring full (K, or staged codes of V) and, block by
+        // block, converts its half of V. The copies run ahead with a walk of
+        // their own; block i's slot is free once block i - nslot has been used,
+        // which no later block's V is needed for.
+        ChWalk ld(p, d, tpt);
+        int lj = ld.kb;
+        uint32_t issued = 0, it = 0;
+        for (ChWalk w(p, d, tpt); ok && w.valid(); w.next()) {
+          for (int j = w.kb; j < w.ke && ok; ++j, ++it) {
+            for (; ok && ld.valid() && issued < it + nslot; ++issued) {
+              const uint32_t s = issued % nslot;
+              if (issued >= nslot)
+                ok = __all_sync(0xffffffffu, paged_wait(bEmpty + 8 * s, ((issued / nslot) - 1) & 1, abort_flag));
+              if (!ok) break;
+              copy_block(ld, lj, s, bFull + 8 * s);
+              if (++lj >= ld.ke) {
+                ld.next();
+                lj = ld.kb;
+              }
+            }
+            if (!ok) break;
+            const uint32_t cs = it % C::STAGES, s = it % C::SV;
+            ok = paged_wait(bCFull + 8 * cs, (it / C::STAGES) & 1, abort_flag);
+            if (ok && it >= C::SV) ok = paged_wait(bVEmpty + 8 * s, ((it / C::SV) - 1) & 1, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            ch_convert_v(reinterpret_cast<const uint4*>(gen + (sVc - base) + cs * C::VC_BYTES), sV + s * C::V_BYTES,
+                         is_k ? 0 : 1, lane, w.r.kv - j * kChN);
+            fence_proxy_async_smem();
+            mbar_arrive(bCEmpty + 8 * cs);
+            mbar_arrive(bVFull + 8 * s);
+          }
+        }
       }
+      if (!ok) __nanosleep(200000);  // copies in flight land before the block ends
       __syncwarp();
     } else {
       // ---------------------------------------------------------- MMA issuers: warp 1 S = Q K^T, warp 2 O += P V
@@ -477,10 +520,13 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
                 ++ns;
                 tc_fence_after();
                 const uint32_t a_lo = q_lo0 + t * (C::Q_BYTES >> 4), b_lo = k_lo0 + s * (C::K_BYTES >> 4);
+                // 32 bytes of each row per step: 16 bf16, or 32 codes (Q's first and second halves
+                // against the same K)
 #pragma unroll
-                for (int kk = 0; kk < DQK / 16; ++kk) {
-                  const uint32_t off = ((kk / 4) * C::CHUNK + (kk % 4) * 32) >> 4;
-                  mma_ss_lo<false>(tmem, a_lo + off, b_lo + off, C::IDESC_QK, kk > 0 ? 1u : 0u);
+                for (int kk = 0; kk < 2 * DQK / 32; ++kk) {
+                  const int kb = FP8 ? kk % (DQK / 32) : kk;
+                  mma_ss_lo<FP8>(tmem, a_lo + (((kk / 4) * C::CHUNK + (kk % 4) * 32) >> 4),
+                                 b_lo + (((kb / 4) * C::CHUNK + (kb % 4) * 32) >> 4), C::IDESC_QK, kk > 0 ? 1u : 0u);
                 }
                 tc_commit(bSFull + 8 * t);
                 if (j == e - 1) tc_commit(bQEmpty + 8 * t);
@@ -524,7 +570,7 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
       }
       __syncwarp();
     }
-  } else if (warp < 12) {
+  } else {
     setmaxnreg_inc<C::REGS_SOFT>();
     // ------------------------------------------------------------ softmax and epilogue, one thread per row
     const int t = (warp - 4) >> 2;
@@ -562,7 +608,8 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
         continue;
       }
       if constexpr (FP8) {
-        // this row of Q as fp16, its largest element brought to [1/2, 1)
+        // this row of Q as two e4m3 numbers per element, side by side: codes
+        // [0, d) nearest, [d, 2 d) the rest
         constexpr int W = DQK / 2;
         uint32_t q[W];
         const uint4* src = reinterpret_cast<const uint4*>(
@@ -577,20 +624,33 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
         for (int i = 0; i < W; ++i)
           amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(q[i] << 16)), fabsf(__uint_as_float(q[i] & 0xffff0000u))));
         int e = 0;
-        if (amax > 0.0f && amax < INFINITY) e = max(-126, min(126, static_cast<int>(__float_as_uint(amax) >> 23) - 126));
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        if (amax > 0.0f && amax < INFINITY)
+          e = max(-118, min(126, static_cast<int>(__float_as_uint(amax) >> 23) - 134));
+        float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        if (amax == INFINITY) down = __uint_as_float(0x7fffffffu);  // an infinite element: NaN scores
         c_log2 *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * __ldg(p.k_scale + w.h);
         if (units > 0) ok = paged_wait(bQEmpty + 8 * t, (units - 1) & 1, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+        const uint32_t row = sQ + t * C::Q_BYTES + r * 128;
 #pragma unroll
-        for (int i = 0; i < W / 4; ++i) {
-          uint32_t y[4];
+        for (int i = 0; i < W / 8; ++i) {  // 16 elements
+          uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int n = 0; n < 4; ++n)
-            y[n] = pack_f16x2(__uint_as_float(q[4 * i + n] << 16) * down, __uint_as_float(q[4 * i + n] & 0xffff0000u) * down);
-          st_shared_v4(sQ + t * C::Q_BYTES + (i >> 3) * C::CHUNK + r * 128 + (((i & 7) ^ (r & 7)) << 4), y[0], y[1], y[2],
-                       y[3]);
+          for (int n = 0; n < 4; ++n) {
+            const uint32_t a = q[8 * i + 2 * n], b = q[8 * i + 2 * n + 1];
+            const float f0 = __uint_as_float(a << 16) * down, f1 = __uint_as_float(a & 0xffff0000u) * down;
+            const float f2 = __uint_as_float(b << 16) * down, f3 = __uint_as_float(b & 0xffff0000u) * down;
+            const uint32_t h01 = pack_e4m3x2(f0, f1), h23 = pack_e4m3x2(f2, f3);
+            const float2 g01 = __half22float2(bits_half2(e4m3x2_f16x2(h01)));
+            const float2 g23 = __half22float2(bits_half2(e4m3x2_f16x2(h23)));
+            hi[n] = h01 | (h23 << 16);
+            lo[n] = static_cast<uint32_t>(pack_e4m3x2(f0 - g01.x, f1 - g01.y)) |
+                    (static_cast<uint32_t>(pack_e4m3x2(f2 - g23.x, f3 - g23.y)) << 16);
+          }
+          const int uh = i, ul = DQK / 16 + i;  // 16-byte units of the row
+          st_shared_v4(row + (uh >> 3) * C::CHUNK + (((uh & 7) ^ (r & 7)) << 4), hi[0], hi[1], hi[2], hi[3]);
+          st_shared_v4(row + (ul >> 3) * C::CHUNK + (((ul & 7) ^ (r & 7)) << 4), lo[0], lo[1], lo[2], lo[3]);
         }
         fence_proxy_async_smem();
         mbar_arrive(bQFull + 8 * t);
@@ -748,42 +808,6 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
       }
       tc_fence_before();
       mbar_arrive(bOEmpty + 8 * t);
-    }
-  } else {
-    // ------------------------------------------------------------ e4m3 -> fp16 tiles
-    if constexpr (FP8) {
-      setmaxnreg_dec<C::REGS_CONV>();
-      const int tid = threadIdx.x - 384;
-      const uint4* kc = reinterpret_cast<const uint4*>(gen + (sKc - base));
-      const uint4* vc = reinterpret_cast<const uint4*>(gen + (sVc - base));
-      uint32_t it = 0;
-      bool ok = true;
-      // staged codes -> registers -> fp16 tile, once the tile's last products are done
-      auto turn = [&](auto& regs, const uint4* staged, int which, uint32_t bFull, uint32_t bEmpty, uint32_t dst, int n,
-                      int keys, uint32_t bytes) {
-        const uint32_t s = it % n;
-        ok = __all_sync(0xffffffffu, paged_wait(bCFull + 8 * which, it & 1, abort_flag));
-        if (!ok) return;
-        regs.load(staged, tid);
-        mbar_arrive(bCEmpty + 8 * which);
-        if (it >= static_cast<uint32_t>(n))
-          ok = __all_sync(0xffffffffu, paged_wait(bEmpty + 8 * s, ((it / n) - 1) & 1, abort_flag));
-        if (!ok) return;
-        regs.store(dst + s * bytes, tid, keys);
-        fence_proxy_async_smem();
-        mbar_arrive(bFull + 8 * s);
-      };
-      for (ChWalk w(p, d, tpt); ok && w.valid(); w.next()) {
-        for (int j = w.kb; j < w.ke && ok; ++j, ++it) {
-          {
-            ChRegs<DQK> kr;
-            turn(kr, kc, 0, bKFull, bKEmpty, sK, C::SK, kChN, C::K_BYTES);  // masked scores need no clean keys
-          }
-          if (!ok) break;
-          ChRegs<DV> vr;
-          turn(vr, vc, 1, bVFull, bVEmpty, sV, C::SV, w.r.kv - j * kChN, C::V_BYTES);
-        }
-      }
     }
   }
 
