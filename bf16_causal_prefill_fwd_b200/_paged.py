@@ -9,125 +9,134 @@ are contiguous, the other strides are multiples of 16 bytes.
 
 Lengths, tables and slots are int32 CUDA tensors read on the device only: no call
 here copies from the device or waits for it, so each can be captured into a CUDA
-graph and replayed on new contents.
+graph and replayed on new contents. Work goes to the current stream of the
+tensors' device, whichever device is current.
+
+A decoding step makes these calls once per layer, with kernels of a few
+microseconds, so the checks read each tensor's properties once and build error
+texts only when they fail.
 """
 from __future__ import annotations
 
-import contextlib
 import struct
 
 import torch
 
 from . import _binding as _b
 
-_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
-# b200attn_paged_cache of the header
-_CACHE = struct.Struct("@2P6q6i2P")
+_BF16, _F32, _I32, _U8, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
+_CACHE = struct.Struct("@2P6q6i2P")  # b200attn_paged_cache of the header
+_device_of = torch.Tensor.get_device  # -1: not on a GPU
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _is_cuda(t):
-    return isinstance(t, torch.Tensor) and t.is_cuda
+def _need(ok, name, what, t):
+    if not ok:
+        got = f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor) else type(t).__name__
+        raise ValueError(f"{name} must be {what}, got {got}")
 
 
-def _check_ints(name, t, shape, device):
-    if not (_is_cuda(t) and t.dtype is _I32 and t.shape == shape and t.device == device and t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on {device}")
+def _ints(name, t, shape, dev):
+    """Address of a contiguous int32 tensor of `shape` on GPU `dev`."""
+    try:
+        if t.dtype is _I32 and t.shape == shape and _device_of(t) == dev and t.is_contiguous():
+            return t.data_ptr()
+    except (AttributeError, TypeError):
+        pass
+    _need(False, name, f"a contiguous int32 tensor of shape {tuple(shape)} on cuda:{dev}", t)
 
 
-def _check_table(t, batch, device):
-    """The row stride of a block table."""
-    if not (_is_cuda(t) and t.dtype is _I32 and t.dim() == 2 and t.device == device):
-        raise ValueError(f"block_table must be a 2-D int32 tensor on {device}")
-    (rows, width), (row, col) = t.shape, t.stride()
-    if rows != batch or width < 1:
-        raise ValueError(f"block_table must have shape [{batch}, pages], got {tuple(t.shape)}")
-    if rows == 1:
-        row = width
-    if (width > 1 and col != 1) or row < width:
-        raise ValueError("block_table must have contiguous rows that do not overlap")
-    return row
+def _batch(name, t):
+    """(batch, device) of an int32 [batch] tensor."""
+    try:
+        dev = _device_of(t)
+        if dev >= 0 and t.dtype is _I32 and t.dim() == 1 and t.shape[0] > 0:
+            return t.shape[0], dev
+    except (AttributeError, TypeError):
+        pass
+    _need(False, name, "a contiguous int32 [batch] CUDA tensor", t)
 
 
-def _check_rows(name, t, heads, d, device):
-    """bf16 [tokens, heads, d], each token contiguous, tokens any multiple of 8
-    elements apart (a slice of a fused projection's output): their distance."""
-    if not (_is_cuda(t) and t.dtype is _BF16 and t.dim() == 3 and t.device == device):
-        raise ValueError(f"{name} must be a 3-D bf16 tensor on {device}")
-    (_, h, dim), (token, head, one) = t.shape, t.stride()
-    if (heads is not None and h != heads) or h < 1 or dim != d:
-        raise ValueError(f"{name} must have shape [tokens, {heads or 'heads'}, {d}], got {tuple(t.shape)}")
-    if one != 1 or (h > 1 and head != d) or token % 8 != 0:
-        raise ValueError(f"{name} must have contiguous heads and a token stride that is a multiple of 8 elements")
-    return token
+def _table(t, batch, dev):
+    """(row stride, width) of a block table."""
+    try:
+        if t.dtype is _I32 and _device_of(t) == dev:
+            (rows, width), (row, col) = t.shape, t.stride()
+            if rows == 1:
+                row = width
+            if rows == batch and width > 0 and (col == 1 or width == 1) and row >= width:
+                return row, width
+    except (AttributeError, TypeError, ValueError):
+        pass
+    _need(False, "block_table", f"int32 [{batch}, pages] on cuda:{dev} with contiguous rows that do not overlap", t)
 
 
-def _strides(name, c, esz):
-    """(page, token, head) strides in elements; those of dimensions of one are replaced by what they would be."""
-    (P, ps, H, d), (page, token, head, one) = c.shape, c.stride()
-    if P == 1:
-        page = ps * H * d
-    if ps == 1:
-        token = H * d
-    if H == 1:
-        head = d
-    if one != 1:
-        raise ValueError(f"{name} must have contiguous rows (d fastest)")
-    if page <= 0 or token <= 0 or head <= 0 or (page | token | head) * esz & 15:
-        raise ValueError(f"{name}'s strides must be positive multiples of 16 bytes")
-    return page, token, head
+def _rows(name, t, d, dev):
+    """(tokens, heads, distance of tokens) of bf16 [tokens, heads, d], each token contiguous, tokens any multiple of 8
+    elements apart (a slice of a fused projection's output)."""
+    try:
+        if t.dtype is _BF16 and _device_of(t) == dev:
+            (n, h, dim), (token, head, one) = t.shape, t.stride()
+            if dim == d and h > 0 and one == 1 and (head == d or h == 1) and token % 8 == 0:
+                return n, h, token
+    except (AttributeError, TypeError, ValueError):
+        pass
+    _need(False, name, f"bf16 [tokens, heads, {d}] on cuda:{dev} with contiguous heads and a token stride that is a "
+                       "multiple of 8 elements", t)
 
 
-def _cache(k_cache, v_cache, k_scale, v_scale):
-    """Checks the cache tensors: (description for the library, Hkv, d_qk, d_v)."""
-    if not (_is_cuda(k_cache) and _is_cuda(v_cache)):
-        raise ValueError("k_cache and v_cache must be CUDA tensors")
-    if k_cache.dim() != 4 or v_cache.dim() != 4:
-        raise ValueError("k_cache and v_cache must be 4-D [pages, page_size, H, d]")
-    dev, dtype = k_cache.device, k_cache.dtype
-    (P, ps, H, d_qk), d_v = k_cache.shape, v_cache.shape[3]
-    if v_cache.device != dev:
-        raise ValueError("k_cache and v_cache must be on one device")
-    if v_cache.shape != (P, ps, H, d_v) or v_cache.dtype is not dtype:
-        raise ValueError("k_cache and v_cache must agree in pages, page_size, heads and dtype")
-    if P < 1 or ps < 1 or H < 1:
-        raise ValueError("the cache must hold at least one page, row and head")
+def _cache(k, v, k_scale, v_scale):
+    """Checks the cache tensors: (description for the library, device, Hkv, d_qk, d_v)."""
+    try:
+        dev, dtype = _device_of(k), k.dtype
+        (P, ps, H, d_qk), (page, token, head, one) = k.shape, k.stride()
+        (vP, vps, vH, d_v), (vpage, vtoken, vhead, vone) = v.shape, v.stride()
+        fine = dev >= 0 and _device_of(v) == dev and v.dtype is dtype and one == 1 and vone == 1
+    except (AttributeError, TypeError, ValueError):
+        fine = False
+    if not fine:
+        raise ValueError("k_cache and v_cache must be 4-D [pages, page_size, H, d] CUDA tensors of one dtype and device, "
+                         "d fastest")
+    if vP != P or vps != ps or vH != H or P < 1 or ps < 1 or H < 1:
+        raise ValueError("k_cache and v_cache must agree in pages, page_size and heads, at least one of each")
     if dtype is _BF16:
         if k_scale is not None or v_scale is not None:
             raise ValueError("scales are for e4m3 caches")
         esz, code, ks, vs = 2, _b.BF16, 0, 0
-    elif _b._is_fp8(k_cache):
+    elif dtype is _E4M3 or dtype is _U8:
         for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
             if s is None:
                 raise ValueError(f"{name} is required for an e4m3 cache")
-            if not (_is_cuda(s) and s.dtype is _F32 and s.shape == (H,) and s.device == dev and s.is_contiguous()):
-                raise ValueError(f"{name} must be contiguous fp32 [{H}] on {dev}")
+            if not (isinstance(s, torch.Tensor) and s.dtype is _F32 and s.shape == (H,) and _device_of(s) == dev
+                    and s.is_contiguous()):
+                _need(False, name, f"contiguous fp32 [{H}] on cuda:{dev}", s)
         esz, code, ks, vs = 1, _b.FP8_E4M3, k_scale.data_ptr(), v_scale.data_ptr()
     else:
         raise ValueError("the cache must be bf16 or e4m3")
-    return _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), *_strides("k_cache", k_cache, esz),
-                       *_strides("v_cache", v_cache, esz), P, ps, H, d_qk, d_v, code, ks, vs), H, d_qk, d_v
+    # a dimension of one may come with any stride: what it would be
+    if P == 1:
+        page, vpage = ps * H * d_qk, ps * H * d_v
+    if ps == 1:
+        token, vtoken = H * d_qk, H * d_v
+    if H == 1:
+        head, vhead = d_qk, d_v
+    if ((page | token | head | vpage | vtoken | vhead) * esz & 15
+            or min(page, token, head, vpage, vtoken, vhead) <= 0):
+        raise ValueError("k_cache's and v_cache's strides must be positive multiples of 16 bytes")
+    return (_CACHE.pack(k.data_ptr(), v.data_ptr(), page, token, head, vpage, vtoken, vhead, P, ps, H, d_qk, d_v, code,
+                        ks, vs), dev, H, d_qk, d_v)
 
 
-_HERE = contextlib.nullcontext()
-
-
-def _on(device):
-    """The tensors' device as the current one."""
-    if device.type != "cuda" or device.index == torch._C._cuda_getDevice():
-        return _HERE
-    return torch.cuda.device(device)
-
-
-def _stream(stream, device):
-    """The stream to launch on: the current one of the tensors' device by default."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
-    return _b._stream_handle(stream)
-
-
-def _done(rc, what):
+def _run(name, fn, dev, stream, *args):
+    """Calls the library with the tensors' device current, on its current stream or `stream`."""
+    if dev == _current_device():
+        rc = fn(*args, _raw_stream(dev) if stream is None else _b._stream_handle(stream))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _raw_stream(dev) if stream is None else _b._stream_handle(stream))
     if rc != 0:
-        raise _b.B200AttnError(rc, what)
+        raise _b.B200AttnError(rc, name)
 
 
 def paged_slots(block_table, context_lens, new_lens, total: int, page_size: int, *, free_pages=None, free_head=None,
@@ -141,60 +150,49 @@ def paged_slots(block_table, context_lens, new_lens, total: int, page_size: int,
     itself, or a new tensor). A step that does not fit is empty, and check() says why: -1 for lengths that do not
     fit, -6 for too few free pages.
     """
-    lib = _b.load_library()
-    if not _is_cuda(context_lens) or context_lens.dim() != 1 or context_lens.shape[0] < 1:
-        raise ValueError("context_lens must be an int32 [batch] CUDA tensor")
-    B, dev = context_lens.shape[0], context_lens.device
-    _check_ints("context_lens", context_lens, (B,), dev)
-    _check_ints("new_lens", new_lens, (B,), dev)
-    row = _check_table(block_table, B, dev)
-    total, page_size = int(total), int(page_size)
+    lib = _b._lib or _b.load_library()
+    B, dev = _batch("context_lens", context_lens)
+    ctx = _ints("context_lens", context_lens, (B,), dev)
+    new = _ints("new_lens", new_lens, (B,), dev)
+    row, width = _table(block_table, B, dev)
     if total < 0 or page_size < 1:
         raise ValueError("total must not be negative and page_size at least 1")
     free, count, head, head_out = None, 0, None, None
     if free_pages is not None:
-        if not _is_cuda(free_pages) or free_pages.dim() != 1:
-            raise ValueError("free_pages must be an int32 [pages] CUDA tensor")
-        count = free_pages.shape[0]
-        _check_ints("free_pages", free_pages, (count,), dev)
-        _check_ints("free_head", free_head, (1,), dev)
+        count = free_pages.numel() if isinstance(free_pages, torch.Tensor) else 0
+        free = _ints("free_pages", free_pages, (count,), dev)
+        head = _ints("free_head", free_head, (1,), dev)
+        if count == 0:
+            free = head  # an empty list needs an address; none of it is read
         if free_head_out is not None:
-            _check_ints("free_head_out", free_head_out, (1,), dev)
-        head = free_head.data_ptr()
-        free = free_pages.data_ptr() or head  # an empty list needs an address; none of it is read
+            head_out = _ints("free_head_out", free_head_out, (1,), dev)
     elif free_head is not None or free_head_out is not None:
         raise ValueError("free_head goes with free_pages")
-    out = torch.empty(2 * B + 2 + 2 * total, dtype=_I32, device=dev)
+    # one allocation: int32 cu_seqlens, kv_lens, positions, slots, head
+    out = context_lens.new_empty(2 * B + 2 + 2 * total)
     cu, kv, pos, slots, new_head = out.split_with_sizes((B + 1, B, total, total, 1))
     at = out.data_ptr()
-    if free_pages is not None:
-        if free_head_out is None:
-            free_head_out = new_head
-        head_out = free_head_out.data_ptr()
-    with _on(dev):
-        _done(lib.b200attn_paged_slots(
-            block_table.data_ptr(), row, block_table.shape[1], context_lens.data_ptr(), new_lens.data_ptr(), B, total,
-            page_size, free, count, head, head_out, at, at + 4 * (B + 1), at + 4 * (2 * B + 1),
-            at + 4 * (2 * B + 1 + total), _stream(stream, dev)), "b200attn_paged_slots")
-    return (cu, kv, pos, slots) if free_pages is None else (cu, kv, pos, slots, free_head_out)
+    if free is not None and free_head_out is None:
+        free_head_out, head_out = new_head, at + 4 * (2 * B + 1 + 2 * total)
+    _run("b200attn_paged_slots", lib.b200attn_paged_slots, dev, stream, block_table.data_ptr(), row, width, ctx, new, B,
+         total, page_size, free, count, head, head_out, at, at + 4 * (B + 1), at + 4 * (2 * B + 1),
+         at + 4 * (2 * B + 1 + total))
+    return (cu, kv, pos, slots) if free is None else (cu, kv, pos, slots, free_head_out)
 
 
 def paged_append_kv(k, v, k_cache, v_cache, slots, *, k_scale=None, v_scale=None, stream=None):
     """Writes the rows of k [total, Hkv, d_qk] and v [total, Hkv, d_v] (bf16; slices of a fused projection's output
     are taken as they are) to the cache rows ``slots`` (int32 [total]; negative: the row is skipped), as bf16 or as
     e4m3(x / scale) with one fp32 scale per head, via b200attn_paged_append. Returns (k_cache, v_cache)."""
-    lib = _b.load_library()
-    cache, H, d_qk, d_v = _cache(k_cache, v_cache, k_scale, v_scale)
-    dev = k_cache.device
-    k_row = _check_rows("k", k, H, d_qk, dev)
-    v_row = _check_rows("v", v, H, d_v, dev)
-    total = k.shape[0]
-    if v.shape[0] != total:
-        raise ValueError("k and v must have the same number of tokens")
-    _check_ints("slots", slots, (total,), dev)
-    with _on(dev):
-        _done(lib.b200attn_paged_append(k.data_ptr(), v.data_ptr(), k_row, v_row, total, cache, slots.data_ptr(),
-                                        _stream(stream, dev)), "b200attn_paged_append")
+    lib = _b._lib or _b.load_library()
+    cache, dev, H, d_qk, d_v = _cache(k_cache, v_cache, k_scale, v_scale)
+    total, kh, k_row = _rows("k", k, d_qk, dev)
+    vn, vh, v_row = _rows("v", v, d_v, dev)
+    if kh != H or vh != H or vn != total:
+        raise ValueError(f"k and v must have the cache's {H} heads and the same number of tokens")
+    at = _ints("slots", slots, (total,), dev)
+    _run("b200attn_paged_append", lib.b200attn_paged_append, dev, stream, k.data_ptr(), v.data_ptr(), k_row, v_row, total,
+         cache, at)
     return k_cache, v_cache
 
 
@@ -213,43 +211,35 @@ def attn_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, *, max
     at most 16 / (Hq / Hkv) of them the decoding kernel runs. Returns bf16 [total, Hq, d_v] (and fp32 lse
     [Hq, total]); rows of no request are left unwritten.
     """
-    lib = _b.load_library()
-    cache, Hkv, d_qk, d_v = _cache(k_cache, v_cache, k_scale, v_scale)
-    dev = k_cache.device
-    q_row = _check_rows("q", q, None, d_qk, dev)
-    total, Hq, _ = q.shape
+    lib = _b._lib or _b.load_library()
+    cache, dev, Hkv, d_qk, d_v = _cache(k_cache, v_cache, k_scale, v_scale)
+    total, Hq, q_row = _rows("q", q, d_qk, dev)
     if Hq % Hkv != 0:
         raise ValueError("the query heads must be a multiple of the cache's heads")
-    if not _is_cuda(kv_lens) or kv_lens.dim() != 1 or kv_lens.shape[0] < 1:
-        raise ValueError("kv_lens must be an int32 [batch] CUDA tensor")
-    B = kv_lens.shape[0]
-    _check_ints("kv_lens", kv_lens, (B,), dev)
-    _check_ints("cu_seqlens", cu_seqlens, (B + 1,), dev)
-    row = _check_table(block_table, B, dev)
-    max_q = total if max_seqlen_q is None else int(max_seqlen_q)
+    B, _ = _batch("kv_lens", kv_lens)
+    kv = _ints("kv_lens", kv_lens, (B,), dev)
+    cu = _ints("cu_seqlens", cu_seqlens, (B + 1,), dev)
+    row, width = _table(block_table, B, dev)
+    max_q = total if max_seqlen_q is None else min(int(max_seqlen_q), total)
     if max_q < 1 and total > 0:
         raise ValueError("max_seqlen_q must be at least 1")
     if out is None:
-        out = torch.empty((total, Hq, d_v), dtype=_BF16, device=dev)
+        out = q.new_empty((total, Hq, d_v))
     else:
-        _b._check_buffer("out", out, (total, Hq, d_v), (_BF16,), dev)
-    lse = torch.empty((Hq, total), dtype=_F32, device=dev) if return_lse else None
+        _b._check_buffer("out", out, (total, Hq, d_v), (_BF16,), q.device)
+    lse = torch.empty((Hq, total), dtype=_F32, device=q.device) if return_lse else None
     if total == 0:
         return (out, lse) if return_lse else out
-    max_q = min(max_q, total)
     if workspace is None:
         size = lib.b200attn_paged_fwd_workspace_bytes(total, max_q, Hq, Hkv)
-        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        workspace = kv_lens.new_empty((size + 3) // 4)
     else:
-        if not _is_cuda(workspace) or workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be contiguous on {dev}")
+        if not isinstance(workspace, torch.Tensor) or _device_of(workspace) != dev or not workspace.is_contiguous():
+            _need(False, "workspace", f"contiguous on cuda:{dev}", workspace)
         size = workspace.numel() * workspace.element_size()
-    with _on(dev):
-        _done(lib.b200attn_paged_fwd(
-            q.data_ptr(), q_row, cache, block_table.data_ptr(), row, block_table.shape[1], cu_seqlens.data_ptr(),
-            kv_lens.data_ptr(), B, total, max_q, Hq, 1 if causal else 0, float(softmax_scale) if softmax_scale else 0.0,
-            out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(), size, _stream(stream, dev)),
-              "b200attn_paged_fwd")
+    _run("b200attn_paged_fwd", lib.b200attn_paged_fwd, dev, stream, q.data_ptr(), q_row, cache, block_table.data_ptr(), row,
+         width, cu, kv, B, total, max_q, Hq, 1 if causal else 0, float(softmax_scale) if softmax_scale else 0.0,
+         out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(), size)
     return (out, lse) if return_lse else out
 
 

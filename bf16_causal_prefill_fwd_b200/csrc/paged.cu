@@ -236,7 +236,7 @@ int launch_chunk(const b200attn_paged_cache* c, PagedAttn p, int sm_count, int d
   const int blocks = sm_count < b200p::kChMaxBlocks ? sm_count : b200p::kChMaxBlocks;
   kern<<<blocks, C::THREADS, C::SMEM, st>>>(tq, tk, tv, p);
   if (cudaGetLastError() != cudaSuccess) return B200ATTN_ERR_CUDA;
-  return launch_dependent(b200p::paged_join_kernel<128>, dim3(blocks, p.slot_rows < 64 ? (p.slot_rows + 3) / 4 : 16, 1), 128, st, static_cast<const PagedAttn>(p));
+  return launch_dependent(b200p::paged_join_kernel<128>, dim3(blocks, p.slot_rows < 16 ? 4 : 16, 1), 128, st, static_cast<const PagedAttn>(p));
 }
 
 }  // namespace

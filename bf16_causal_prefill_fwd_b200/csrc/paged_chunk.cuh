@@ -35,7 +35,7 @@
 // would need the same split in the softmax, the busiest warps here; instead V's
 // codes become fp16 (exactly) in shared memory, by the two copying warps, and P
 // is fp16. Converting K as well, with four more warps, took 503 us where this
-// takes 390 (4 requests of 500-1300 new tokens, 2-12k keys).
+// takes 395 (4 requests of 500-1300 new tokens, 2-12k keys).
 //
 // Bound by the tensor core (2 x 2 x 128^3 products per key block and pair) and,
 // for chunks of a few tokens, by reading the cache.
