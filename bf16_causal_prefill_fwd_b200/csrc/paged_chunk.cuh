@@ -75,7 +75,7 @@ struct ChCfg {
   static constexpr int SK_FIT = (AVAIL - SV * V_BYTES) / K_BYTES, SK = SK_FIT > 4 ? 4 : SK_FIT;
   static constexpr int BARS = 2 + 2 + 2 * SK + 2 * SV + 1 + 4 + 2 + 1 + 2 + 2 + 2 + 2 + 2;
   static constexpr int SMEM = 2 * Q_BYTES + SK * K_BYTES + SV * V_BYTES + STAGES * VC_BYTES + 1024 + 1024;
-  static_assert(8 * BARS + 8 <= 512 && 512 + 8 * 64 <= 1024 && SMEM <= 227 * 1024 && SK >= 2, "shared memory");
+  static_assert(8 * BARS + 8 + 32 <= 512 && 512 + 8 * 64 <= 1024 && SMEM <= 227 * 1024 && SK >= 2, "shared memory");
   // Tensor memory: S [0, 128) for both tiles in turn, O_t at 128 + 128 t, P_t
   // (16-bit, 64 columns) at 384 + 64 t.
   static constexpr int TM_O = 128, TM_P = 384;
@@ -188,24 +188,35 @@ __device__ __forceinline__ ChStart ch_start(const PagedAttn& p, int tpt, int* sm
 
 // Walks the pieces of a block's run: key blocks [kb, ke) of unit (b, h, pair).
 // A unit takes kChUnitCost + (its key blocks) of the line, the cost first.
+// The piece that begins inside a unit comes last, so that every block starts a
+// unit at key 0 at the same time: blocks of one key/value head then go over its
+// keys together and share them in L2 (one chunk of 4096 tokens over 28k keys read
+// 2.7 GB from HBM with the pieces in order, %%% GB so).
 struct ChWalk {
   const PagedAttn& p;
+  const ChStart* start;  // shared memory
+  bool later;            // the first piece is still to come
   Request r;
   int b, h, pair, tpt;
   int kb, ke, n0, n1;  // this piece; key blocks of the unit's tiles
   int left, at;        // what is left of the run after this piece; the unit's place in the line
-  __device__ ChWalk(const PagedAttn& params, const ChStart& d, int tokens) : p(params), tpt(tokens) {
-    b = d.b;
-    h = d.h;
-    pair = d.pair;
-    left = d.count;
-    at = d.first - d.skip;
-    kb = ke = n0 = n1 = 0;
-    if (left > 0) {
-      r = paged_request(p, b, false);
-      take(d.skip);
-      if (!valid()) next();
+  __device__ ChWalk(const PagedAttn& params, const ChStart* s, int tokens)
+      : p(params), start(s), later(false), tpt(tokens) {
+    kb = ke = 0;
+    if (s->count > 0) {
+      begin();
+      later = kb > 0;
+      if (later || !valid()) next();
     }
+  }
+  __device__ void begin() {
+    b = start->b;
+    h = start->h;
+    pair = start->pair;
+    left = start->count;
+    at = start->first - start->skip;
+    r = paged_request(p, b, false);
+    take(start->skip);
   }
   // The softmax warps keep a whole score row in registers; what the walk needs
   // is put into shared memory (64 bytes per warp, every lane the same) while the
@@ -214,11 +225,15 @@ struct ChWalk {
     st_shared_v4(at_smem, b, h, pair, left);
     st_shared_v4(at_smem + 16, at, kb, ke, n0);
     st_shared_v4(at_smem + 32, n1, r.t0, r.nq, r.kv);
+    st_shared_v4(at_smem + 48, later, 0, 0, 0);
   }
   __device__ void get(uint32_t at_smem) {
     ld_shared_v4(at_smem, b, h, pair, left);
     ld_shared_v4(at_smem + 16, at, kb, ke, n0);
     ld_shared_v4(at_smem + 32, n1, r.t0, r.nq, r.kv);
+    int x, y, z, f;
+    ld_shared_v4(at_smem + 48, f, x, y, z);
+    later = f != 0;
   }
   __device__ void take(int skip) {
     n0 = ch_blocks(r, 2 * pair, tpt, p.causal);
@@ -237,14 +252,21 @@ struct ChWalk {
     do {
       at += max(n0, n1) + kChUnitCost;
       kb = ke = 0;
-      if (left == 0) return;
+      if (left == 0) {
+        if (later) {
+          begin();
+          left = 0;
+          later = false;
+        }
+        return;
+      }
       if (++pair == ch_pairs(r, tpt)) {
         pair = 0;
         if (++h == p.Hkv) {
           h = 0;
           do {  // more is left, so a request with tokens follows
             if (++b >= p.B) {
-              left = 0;
+              left = later = 0;
               return;
             }
             r = paged_request(p, b, false);
@@ -388,7 +410,9 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
     tmem_alloc(smem_addr(tmem_slot), 512);
     tmem_relinquish();
   }
+  ChStart* start = reinterpret_cast<ChStart*>(bar_gen + 8 * C::BARS + 8);
   const ChStart d = ch_start<C::THREADS>(p, tpt, reinterpret_cast<int*>(gen));  // in the Q buffers, not in use yet
+  if (threadIdx.x == 0) *start = d;
   fence_proxy_async_smem();  // TMA writes there next
   tc_fence_before();
   __syncthreads();
@@ -427,7 +451,7 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
       };
       if constexpr (!FP8) {
         uint32_t it = 0, tails = 0, nq[2] = {0, 0};
-        for (ChWalk w(p, d, tpt); ok && w.valid(); w.next()) {
+        for (ChWalk w(p, start, tpt); ok && w.valid(); w.next()) {
           if (is_k) {
             for (int t = 0; t < 2 && ok; ++t) {
               if (!w.has(t)) continue;
@@ -468,10 +492,10 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
         // block, converts its half of V. The copies run ahead with a walk of
         // their own; block i's slot is free once block i - nslot has been used,
         // which no later block's V is needed for.
-        ChWalk ld(p, d, tpt);
+        ChWalk ld(p, start, tpt);
         int lj = ld.kb;
         uint32_t issued = 0, it = 0;
-        for (ChWalk w(p, d, tpt); ok && w.valid(); w.next()) {
+        for (ChWalk w(p, start, tpt); ok && w.valid(); w.next()) {
           for (int j = w.kb; j < w.ke && ok; ++j, ++it) {
             for (; ok && ld.valid() && issued < it + nslot; ++issued) {
               const uint32_t s = issued % nslot;
@@ -506,7 +530,7 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
         const uint32_t q_lo0 = sdesc_lo(sQ, 16), k_lo0 = sdesc_lo(sK, 16), v_lo0 = sdesc_lo(sV, C::CHUNK);
         uint32_t it = 0, ns = 0, cnt[2] = {0, 0}, g[2] = {0, 0};
         bool ok = true;
-        for (ChWalk w(p, d, tpt); ok && w.valid(); w.next()) {
+        for (ChWalk w(p, start, tpt); ok && w.valid(); w.next()) {
           if (warp == 1) {
             for (int t = 0; t < 2 && ok; ++t)
               if (w.has(t)) ok = paged_wait(bQFull + 8 * t, cnt[t]++ & 1, abort_flag);
@@ -580,7 +604,7 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
     const uint32_t sWalk = sBar + 512 + 64 * (warp - 4);
     uint32_t g = 0, units = 0;  // key blocks and pieces this tile has done
     bool ok = true;
-    for (ChWalk w(p, d, tpt); ok && w.valid(); w.next()) {
+    for (ChWalk w(p, start, tpt); ok && w.valid(); w.next()) {
       float c_log2 = p.scale_log2;
       int see, see_all, end;
       {
@@ -590,7 +614,7 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
       const bool whole = w.whole(), head = w.kb > 0;
       if (t == 0 && r == 0 && !whole && !head) {
         PartDesc e;
-        e.last = w.last() / d.per;
+        e.last = w.last() / start->per;
         e.t0 = w.r.t0;
         e.row0 = 2 * w.pair * tpt * p.G;
         e.nrows = min(2 * tpt, w.r.nq - 2 * w.pair * tpt) * p.G;
