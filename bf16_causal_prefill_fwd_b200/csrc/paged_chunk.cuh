@@ -56,6 +56,8 @@ constexpr int kChRows = 2 * kChM;
 constexpr int kChUnitCost = 3;
 constexpr int kChMaxBlocks = 160;  // workspace slots are sized for this many blocks
 
+constexpr int kChUnits = 8;  // units the K warp may be ahead by; more than the blocks its ring holds
+
 template <int DQK, int DV, bool FP8>
 struct ChCfg {
   static constexpr int THREADS = 384, REGS_LAUNCH = 168;
@@ -73,9 +75,9 @@ struct ChCfg {
   static constexpr int PAIRS = AVAIL / (K_BYTES + V_BYTES);
   static constexpr int SV = PAIRS >= 2 ? 2 : 1;
   static constexpr int SK_FIT = (AVAIL - SV * V_BYTES) / K_BYTES, SK = SK_FIT > 4 ? 4 : SK_FIT;
-  static constexpr int BARS = 2 + 2 + 2 * SK + 2 * SV + 1 + 4 + 2 + 1 + 2 + 2 + 2 + 2 + 2;
+  static constexpr int BARS = 2 + 2 + 2 * SK + 2 * SV + 1 + 4 + 2 + 1 + 2 + 2 + 2 + 2 + 2 + 2 * kChUnits;
   static constexpr int SMEM = 2 * Q_BYTES + SK * K_BYTES + SV * V_BYTES + STAGES * VC_BYTES + 1024 + 1024;
-  static_assert(8 * BARS + 8 + 32 <= 512 && 512 + 8 * 64 <= 1024 && SMEM <= 227 * 1024 && SK >= 2, "shared memory");
+  static_assert(8 * BARS + 8 + 32 <= 512 && 512 + kChUnits * 64 <= 1024 && SMEM <= 227 * 1024 && SK >= 2, "shared memory");
   // Tensor memory: S [0, 128) for both tiles in turn, O_t at 128 + 128 t, P_t
   // (16-bit, 64 columns) at 384 + 64 t.
   static constexpr int TM_O = 128, TM_P = 384;
@@ -191,7 +193,8 @@ __device__ __forceinline__ ChStart ch_start(const PagedAttn& p, int tpt, int* sm
 // The piece that begins inside a unit comes last, so that every block starts a
 // unit at key 0 at the same time: blocks of one key/value head then go over its
 // keys together and share them in L2 (one chunk of 4096 tokens over 28k keys read
-// 2.7 GB from HBM with the pieces in order, %%% GB so).
+// 2.7 GB from HBM with the pieces in order, 0.66 GB so).
+// Only the K warp walks; the other roles read what it finds (ChUnit).
 struct ChWalk {
   const PagedAttn& p;
   const ChStart* start;  // shared memory
@@ -218,23 +221,6 @@ struct ChWalk {
     r = paged_request(p, b, false);
     take(start->skip);
   }
-  // The softmax warps keep a whole score row in registers; what the walk needs
-  // is put into shared memory (64 bytes per warp, every lane the same) while the
-  // keys of a piece go by.
-  __device__ void put(uint32_t at_smem) const {
-    st_shared_v4(at_smem, b, h, pair, left);
-    st_shared_v4(at_smem + 16, at, kb, ke, n0);
-    st_shared_v4(at_smem + 32, n1, r.t0, r.nq, r.kv);
-    st_shared_v4(at_smem + 48, later, 0, 0, 0);
-  }
-  __device__ void get(uint32_t at_smem) {
-    ld_shared_v4(at_smem, b, h, pair, left);
-    ld_shared_v4(at_smem + 16, at, kb, ke, n0);
-    ld_shared_v4(at_smem + 32, n1, r.t0, r.nq, r.kv);
-    int x, y, z, f;
-    ld_shared_v4(at_smem + 48, f, x, y, z);
-    later = f != 0;
-  }
   __device__ void take(int skip) {
     n0 = ch_blocks(r, 2 * pair, tpt, p.causal);
     n1 = ch_blocks(r, 2 * pair + 1, tpt, p.causal);
@@ -244,8 +230,6 @@ struct ChWalk {
     left -= n;
   }
   __device__ bool valid() const { return ke > kb; }
-  __device__ int end(int t) const { return min(ke, t ? n1 : n0); }      // tile t runs blocks [kb, end(t))
-  __device__ bool has(int t) const { return end(t) > kb; }
   __device__ bool whole() const { return kb == 0 && ke == max(n0, n1); }
   __device__ int last() const { return at + kChUnitCost + max(n0, n1) - 1; }  // place of the unit's last key block
   __device__ void next() {
@@ -275,6 +259,31 @@ struct ChWalk {
       }
       take(0);
     } while (!valid());  // the run's end may hold no more than a unit's cost
+  }
+};
+
+// A piece of work as every role of the block sees it, in a ring of shared memory.
+// The K warp fills it as it walks, units ahead of the others: no other role
+// computes or keeps the walk (the softmax warps hold a whole score row each), and
+// none waits for a request's lengths. kb == ke: the end.
+struct ChUnit {
+  int b, h, t0, nq;    // request, key/value head, the request's first row of Q, its new tokens
+  int kv, tok0, kb, ke;  // its keys; first token of tile 0; key blocks [kb, ke)
+  int n0, n1;          // key blocks of the unit's tiles
+  int whole;           // the unit is not split
+  int last;            // the block that has its last piece
+  __device__ int end(int t) const { return min(ke, t ? n1 : n0); }  // tile t runs blocks [kb, end(t))
+  __device__ bool has(int t) const { return end(t) > kb; }
+  __device__ bool valid() const { return ke > kb; }
+  __device__ void put(uint32_t at) const {
+    st_shared_v4(at, b, h, t0, nq);
+    st_shared_v4(at + 16, kv, tok0, kb, ke);
+    st_shared_v4(at + 32, n0, n1, whole, last);
+  }
+  __device__ void get(uint32_t at) {
+    ld_shared_v4(at, b, h, t0, nq);
+    ld_shared_v4(at + 16, kv, tok0, kb, ke);
+    ld_shared_v4(at + 32, n0, n1, whole, last);
   }
 };
 
@@ -371,6 +380,9 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
   const uint32_t bOFull = bPDone + 16;           // [2]
   const uint32_t bOEmpty = bOFull + 16;          // [2]
   const uint32_t bDrain = bOEmpty + 16;          // [2]
+  const uint32_t bUFull = bDrain + 16;           // [kChUnits] a unit is in the ring
+  const uint32_t bUEmpty = bUFull + 8 * kChUnits;  // [kChUnits] every role is done with it
+  const uint32_t sUnit = sBar + 512;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tpt = kChM / p.G;  // tokens per tile
@@ -389,6 +401,10 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
         mbar_init(bDrain + 8 * t, 1);
         mbar_init(bCFull + 8 * t, 1);
         mbar_init(bCEmpty + 8 * t, 64);
+      }
+      for (int i = 0; i < kChUnits; ++i) {
+        mbar_init(bUFull + 8 * i, 1);
+        mbar_init(bUEmpty + 8 * i, FP8 ? 12 : 11);  // the warps that read units
       }
       mbar_init(bSFree, 128);
       mbar_init(bVTail, 1);
@@ -420,10 +436,19 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
   const uint32_t tmem = *tmem_slot;
   if (threadIdx.x == 0) reinterpret_cast<PartDesc*>(p.desc)[blockIdx.x].last = -1;
 
+  // The m-th unit of the block (a whole warp or one thread); the warp says when it
+  // is done with it.
+  auto unit_get = [&](uint32_t m, ChUnit& u) -> bool {
+    const bool got = paged_wait(bUFull + 8 * (m % kChUnits), (m / kChUnits) & 1, abort_flag);
+    u.get(sUnit + 64 * (m % kChUnits));
+    return got;
+  };
+  auto unit_done = [&](uint32_t m) { mbar_arrive(bUEmpty + 8 * (m % kChUnits)); };
+
   if (warp < 4) {
     setmaxnreg_dec<C::REGS_CTRL>();
     if (warp == 0 || warp == 3) {
-      // ---------------------------------------------------------- copies: warp 0 Q and K, warp 3 V
+      // ---------------------------------------------------------- copies: warp 0 K, warp 3 V
       const bool is_k = warp == 0;
       const bool staged = FP8 && !is_k;
       const uint32_t nslot = staged ? C::STAGES : (is_k ? C::SK : C::SV);
@@ -438,75 +463,107 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
       const int box = lane / chunks, c = lane - box * chunks;
       int page = 0;
       bool ok = true;
-      // Block j (the it-th of the ring) of the walk's unit; `bar` counts its bytes.
-      auto copy_block = [&](const ChWalk& w, int j, uint32_t s, uint32_t bar) {
-        const int a = (j - w.kb) % ahead;
-        if (a == 0) page = lane < ahead * boxes ? paged_page(p, w.b, j * kChN + lane * p.box, w.r.kv) : 0;
+      // Block j of request b's head h into slot s; `bar` counts its bytes. `kb`: the piece's first block.
+      auto copy_block = [&](int b, int h, int kv, int kb, int j, uint32_t s, uint32_t bar) {
+        const int a = (j - kb) % ahead;
+        if (a == 0) page = lane < ahead * boxes ? paged_page(p, b, j * kChN + lane * p.box, kv) : 0;
         if (lane == 0) mbar_arrive_expect_tx(bar, slot_bytes);
         __syncwarp();
         const int pg = __shfl_sync(0xffffffffu, page, a * boxes + (lane < issues ? box : 0));
         if (lane < issues)
-          tma_load_4d(ring + s * slot_bytes + c * C::CHUNK + box * p.box * 128, tm, bar, c * (128 / C::KSZ), w.h,
+          tma_load_4d(ring + s * slot_bytes + c * C::CHUNK + box * p.box * 128, tm, bar, c * (128 / C::KSZ), h,
                       (j * kChN + box * p.box) % p.page_size, pg);
       };
+      // Slot of the it-th block, once the block before in it has been used.
+      auto slot_of = [&](uint32_t it) -> uint32_t {
+        const uint32_t s = it % nslot;
+        if (it >= nslot) ok = __all_sync(0xffffffffu, paged_wait(bEmpty + 8 * s, ((it / nslot) - 1) & 1, abort_flag));
+        return s;
+      };
+      // Tells the other roles the m-th unit (K warp).
+      auto publish = [&](const ChWalk& w, uint32_t m) {
+        if (m >= kChUnits)
+          ok = __all_sync(0xffffffffu, paged_wait(bUEmpty + 8 * (m % kChUnits), ((m / kChUnits) - 1) & 1, abort_flag));
+        if (lane == 0) {
+          ChUnit u;
+          u.b = w.b, u.h = w.h, u.t0 = w.r.t0, u.nq = w.r.nq;
+          u.kv = w.r.kv, u.tok0 = 2 * w.pair * tpt, u.kb = w.kb, u.ke = w.ke;
+          u.n0 = w.n0, u.n1 = w.n1, u.whole = w.whole(), u.last = w.valid() ? w.last() / start->per : 0;
+          u.put(sUnit + 64 * (m % kChUnits));
+          mbar_arrive(bUFull + 8 * (m % kChUnits));
+        }
+      };
       if constexpr (!FP8) {
-        uint32_t it = 0, tails = 0, nq[2] = {0, 0};
-        for (ChWalk w(p, start, tpt); ok && w.valid(); w.next()) {
-          if (is_k) {
-            for (int t = 0; t < 2 && ok; ++t) {
-              if (!w.has(t)) continue;
-              if (nq[t] > 0) ok = __all_sync(0xffffffffu, paged_wait(bQEmpty + 8 * t, (nq[t] - 1) & 1, abort_flag));
-              if (!ok) break;
-              ++nq[t];
-              if (lane == 0) {
-                mbar_arrive_expect_tx(bQFull + 8 * t, C::Q_CHUNKS * 128 * tpt * p.G);
-                for (int i = 0; i < C::Q_CHUNKS; ++i)
-                  tma_load_3d(sQ + t * C::Q_BYTES + i * C::CHUNK, &tmQ, bQFull + 8 * t, i * 64, w.h * p.G,
-                              w.r.t0 + (2 * w.pair + t) * tpt);
-              }
+        uint32_t it = 0, m = 0;
+        if (is_k) {
+          ChWalk w(p, start, tpt);
+          for (;; w.next(), ++m) {
+            publish(w, m);
+            if (!ok || !w.valid()) break;
+            for (int j = w.kb; j < w.ke && ok; ++j, ++it) {
+              const uint32_t s = slot_of(it);
+              if (ok) copy_block(w.b, w.h, w.r.kv, w.kb, j, s, bFull + 8 * s);
             }
           }
-          for (int j = w.kb; j < w.ke && ok; ++j, ++it) {
-            const uint32_t s = it % nslot;
-            if (it >= nslot)
-              ok = __all_sync(0xffffffffu, paged_wait(bEmpty + 8 * s, ((it / nslot) - 1) & 1, abort_flag));
-            if (!ok) break;
-            const bool tail = !is_k && (j + 1) * kChN > w.r.kv;
-            copy_block(w, j, s, tail ? bVTail : bFull + 8 * s);
-            if (tail) {
-              ok = __all_sync(0xffffffffu, paged_wait(bVTail, tails & 1, abort_flag));
-              ++tails;
-              const int from = max(0, w.r.kv - j * kChN);
-              for (int i = lane; i < (kChN - from) * C::V_CHUNKS * 8; i += 32) {
-                const int row = from + i / (C::V_CHUNKS * 8), cc = (i / 8) % C::V_CHUNKS;
-                st_shared_v4(ring + s * slot_bytes + cc * C::CHUNK + row * 128 + 16 * (i & 7), 0u, 0u, 0u, 0u);
+        } else {
+          uint32_t tails = 0;
+          ChUnit w;
+          for (; ok; ++m) {
+            ok = __all_sync(0xffffffffu, unit_get(m, w));
+            if (!ok || !w.valid()) break;
+            for (int j = w.kb; j < w.ke && ok; ++j, ++it) {
+              const uint32_t s = slot_of(it);
+              if (!ok) break;
+              const bool tail = (j + 1) * kChN > w.kv;
+              copy_block(w.b, w.h, w.kv, w.kb, j, s, tail ? bVTail : bFull + 8 * s);
+              if (tail) {
+                ok = __all_sync(0xffffffffu, paged_wait(bVTail, tails & 1, abort_flag));
+                ++tails;
+                const int from = max(0, w.kv - j * kChN);
+                for (int i = lane; i < (kChN - from) * C::V_CHUNKS * 8; i += 32) {
+                  const int row = from + i / (C::V_CHUNKS * 8), cc = (i / 8) % C::V_CHUNKS;
+                  st_shared_v4(ring + s * slot_bytes + cc * C::CHUNK + row * 128 + 16 * (i & 7), 0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bFull + 8 * s);
               }
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bFull + 8 * s);
             }
+            __syncwarp();
+            if (lane == 0) unit_done(m);
           }
         }
       } else {
         // Each warp keeps its ring full (K, or staged codes of V) and, block by
-        // block, converts its half of V. The copies run ahead with a walk of
-        // their own; block i's slot is free once block i - nslot has been used,
-        // which no later block's V is needed for.
-        ChWalk ld(p, start, tpt);
-        int lj = ld.kb;
-        uint32_t issued = 0, it = 0;
-        for (ChWalk w(p, start, tpt); ok && w.valid(); w.next()) {
+        // block, converts its half of V. The copies run ahead, with a place in
+        // the units of their own; block i's slot is free once block i - nslot
+        // has been used, which no later block's V is needed for.
+        ChWalk walk(p, start, tpt);  // K warp
+        ChUnit ld, w;
+        uint32_t issued = 0, it = 0, lm = 0, m = 0;
+        int lj = 0;
+        bool more = true;
+        auto ld_unit = [&]() {  // the next unit to copy
+          if (is_k) {
+            if (lm > 0) walk.next();
+            publish(walk, lm);
+            __syncwarp();
+          }
+          ok = ok && __all_sync(0xffffffffu, unit_get(lm, ld));
+          ++lm;
+          more = ok && ld.valid();
+          lj = ld.kb;
+        };
+        ld_unit();
+        for (; ok; ++m) {
+          ok = __all_sync(0xffffffffu, unit_get(m, w));
+          if (!ok || !w.valid()) break;
           for (int j = w.kb; j < w.ke && ok; ++j, ++it) {
-            for (; ok && ld.valid() && issued < it + nslot; ++issued) {
-              const uint32_t s = issued % nslot;
-              if (issued >= nslot)
-                ok = __all_sync(0xffffffffu, paged_wait(bEmpty + 8 * s, ((issued / nslot) - 1) & 1, abort_flag));
+            for (; more && issued < it + nslot; ++issued) {
+              const uint32_t s = slot_of(issued);
               if (!ok) break;
-              copy_block(ld, lj, s, bFull + 8 * s);
-              if (++lj >= ld.ke) {
-                ld.next();
-                lj = ld.kb;
-              }
+              copy_block(ld.b, ld.h, ld.kv, ld.kb, lj, s, bFull + 8 * s);
+              if (++lj >= ld.ke) ld_unit();
             }
             if (!ok) break;
             const uint32_t cs = it % C::STAGES, s = it % C::SV;
@@ -515,11 +572,13 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             ch_convert_v(reinterpret_cast<const uint4*>(gen + (sVc - base) + cs * C::VC_BYTES), sV + s * C::V_BYTES,
-                         is_k ? 0 : 1, lane, w.r.kv - j * kChN);
+                         is_k ? 0 : 1, lane, w.kv - j * kChN);
             fence_proxy_async_smem();
             mbar_arrive(bCEmpty + 8 * cs);
             mbar_arrive(bVFull + 8 * s);
           }
+          __syncwarp();
+          if (lane == 0) unit_done(m);
         }
       }
       if (!ok) __nanosleep(200000);  // copies in flight land before the block ends
@@ -530,16 +589,29 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
         const uint32_t q_lo0 = sdesc_lo(sQ, 16), k_lo0 = sdesc_lo(sK, 16), v_lo0 = sdesc_lo(sV, C::CHUNK);
         uint32_t it = 0, ns = 0, cnt[2] = {0, 0}, g[2] = {0, 0};
         bool ok = true;
-        for (ChWalk w(p, start, tpt); ok && w.valid(); w.next()) {
+        ChUnit w;
+        for (uint32_t m = 0; ok; ++m) {
+          if (!(ok = unit_get(m, w)) || !w.valid()) break;
           if (warp == 1) {
-            for (int t = 0; t < 2 && ok; ++t)
-              if (w.has(t)) ok = paged_wait(bQFull + 8 * t, cnt[t]++ & 1, abort_flag);
+            if constexpr (!FP8) {
+              // Q, once the tile's last products with the one before are done (this thread issued them)
+              for (int t = 0; t < 2; ++t) {
+                if (!w.has(t)) continue;
+                if (cnt[t] > 0 && !(ok = paged_wait(bQEmpty + 8 * t, (cnt[t] - 1) & 1, abort_flag))) break;
+                mbar_arrive_expect_tx(bQFull + 8 * t, C::Q_CHUNKS * 128 * tpt * p.G);
+                for (int i = 0; i < C::Q_CHUNKS; ++i)
+                  tma_load_3d(sQ + t * C::Q_BYTES + i * C::CHUNK, &tmQ, bQFull + 8 * t, i * 64, w.h * p.G,
+                              w.t0 + w.tok0 + t * tpt);
+              }
+              if (!ok) break;
+            }
             for (int j = w.kb; j < w.ke && ok; ++j, ++it) {
               const uint32_t s = it % C::SK;
               if (!(ok = paged_wait(bKFull + 8 * s, (it / C::SK) & 1, abort_flag))) break;
               for (int t = 0; t < 2; ++t) {
                 const int e = w.end(t);
                 if (j >= e) continue;
+                if (j == w.kb && !(ok = paged_wait(bQFull + 8 * t, cnt[t]++ & 1, abort_flag))) break;
                 if (ns > 0 && !(ok = paged_wait(bSFree, (ns - 1) & 1, abort_flag))) break;
                 ++ns;
                 tc_fence_after();
@@ -584,6 +656,7 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
               tc_commit(bVEmpty + 8 * s);
             }
           }
+          if (ok) unit_done(m);
         }
         // every MMA this thread issued has completed before the block frees its tensor memory
         const uint32_t drain = bDrain + 8 * (warp - 1);
@@ -591,6 +664,7 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
         const uint64_t t0 = global_timer_ns();
         while (!mbar_try_wait(drain, 0) && global_timer_ns() - t0 < kPagedWaitLimitNs) {
         }
+        if (!FP8 && warp == 1 && !ok) __nanosleep(200000);  // copies of Q in flight land before the block ends
       }
       __syncwarp();
     }
@@ -601,23 +675,25 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
     const int r = threadIdx.x - 128 - 128 * t;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t tS = tmem + lanes, tO = tmem + lanes + C::TM_O + 128 * t, tP = tmem + lanes + C::TM_P + 64 * t;
-    const uint32_t sWalk = sBar + 512 + 64 * (warp - 4);
     uint32_t g = 0, units = 0;  // key blocks and pieces this tile has done
     bool ok = true;
-    for (ChWalk w(p, start, tpt); ok && w.valid(); w.next()) {
+    ChUnit w;
+    for (uint32_t m = 0; ok; ++m) {
+      ok = __all_sync(0xffffffffu, unit_get(m, w));
+      if (!ok || !w.valid()) break;
       float c_log2 = p.scale_log2;
       int see, see_all, end;
       {
       const int rtok = r / p.G, rhead = r - rtok * p.G;
-      const int tok = (2 * w.pair + t) * tpt + rtok;
-      const bool real = rtok < tpt && tok < w.r.nq;
-      const bool whole = w.whole(), head = w.kb > 0;
+      const int tok = w.tok0 + t * tpt + rtok;
+      const bool real = rtok < tpt && tok < w.nq;
+      const bool whole = w.whole != 0, head = w.kb > 0;
       if (t == 0 && r == 0 && !whole && !head) {
         PartDesc e;
-        e.last = w.last() / start->per;
-        e.t0 = w.r.t0;
-        e.row0 = 2 * w.pair * tpt * p.G;
-        e.nrows = min(2 * tpt, w.r.nq - 2 * w.pair * tpt) * p.G;
+        e.last = w.last;
+        e.t0 = w.t0;
+        e.row0 = w.tok0 * p.G;
+        e.nrows = min(2 * tpt, w.nq - w.tok0) * p.G;
         e.hkv = w.h;
         e.pad[0] = e.pad[1] = e.pad[2] = 0;
         reinterpret_cast<PartDesc*>(p.desc)[blockIdx.x] = e;
@@ -629,6 +705,8 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
           p.part_ml[2 * part] = -INFINITY;
           p.part_ml[2 * part + 1] = 0.0f;
         }
+        __syncwarp();
+        if (lane == 0) unit_done(m);
         continue;
       }
       if constexpr (FP8) {
@@ -637,7 +715,7 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
         constexpr int W = DQK / 2;
         uint32_t q[W];
         const uint4* src = reinterpret_cast<const uint4*>(
-            p.q + (w.r.t0 + (real ? tok : 0)) * p.q_stride + static_cast<int64_t>(w.h * p.G + (real ? rhead : 0)) * DQK);
+            p.q + (w.t0 + (real ? tok : 0)) * p.q_stride + static_cast<int64_t>(w.h * p.G + (real ? rhead : 0)) * DQK);
         float amax = 0.0f;
 #pragma unroll
         for (int i = 0; i < W / 4; ++i) {
@@ -682,12 +760,11 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
       ++units;
       c_log2 = fmaxf(c_log2, 1e-30f);  // a zero scale behaves as a tiny one
       // keys this row sees: j <= see; the tile's first row sees fewest
-      const int off = p.causal ? w.r.kv - w.r.nq : w.r.kv - 1;
-      see = p.causal ? min(off + tok, w.r.kv - 1) : off;
-      see_all = p.causal ? min(off + (2 * w.pair + t) * tpt, w.r.kv - 1) : off;
+      const int off = p.causal ? w.kv - w.nq : w.kv - 1;
+      see = p.causal ? min(off + tok, w.kv - 1) : off;
+      see_all = p.causal ? min(off + w.tok0 + t * tpt, w.kv - 1) : off;
 
       end = w.end(t);
-      w.put(sWalk);
       }
 
       float m_run = -INFINITY, l_run = 0.0f;
@@ -789,17 +866,17 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
       ok = __all_sync(0xffffffffu, paged_wait(bOFull + 8 * t, (units - 1) & 1, abort_flag));
       if (!ok) break;
       tc_fence_after();
-      w.get(sWalk);
+      w.get(sUnit + 64 * (m % kChUnits));  // not kept in registers over the keys
       const int rtok = r / p.G, rhead = r - rtok * p.G;
-      const int tok = (2 * w.pair + t) * tpt + rtok;
-      const bool real = rtok < tpt && tok < w.r.nq;
-      const bool whole = w.whole();
+      const int tok = w.tok0 + t * tpt + rtok;
+      const bool real = rtok < tpt && tok < w.nq;
+      const bool whole = w.whole != 0;
       const int64_t part =
           static_cast<int64_t>(2 * blockIdx.x + (w.kb > 0 ? 0 : 1)) * p.slot_rows + t * tpt * p.G + r;
       const float v_mult = FP8 ? __ldg(p.v_scale + w.h) : 1.0f;
       const float inv = !whole ? 1.0f : (l_run == 0.0f ? 0.0f : v_mult / l_run);
       const int hq = w.h * p.G + rhead;
-      __nv_bfloat16* orow = p.o + (static_cast<int64_t>(w.r.t0 + (real ? tok : 0)) * p.Hq + (real ? hq : 0)) * DV;
+      __nv_bfloat16* orow = p.o + (static_cast<int64_t>(w.t0 + (real ? tok : 0)) * p.Hq + (real ? hq : 0)) * DV;
       float* prow = p.part_o + (real ? part : 0) * DV;
 #pragma unroll 1
       for (int cc = 0; cc < DV; cc += 32) {
@@ -827,11 +904,13 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
         p.part_ml[2 * part] = m_run;
         p.part_ml[2 * part + 1] = l_run;
       } else if (real && p.lse != nullptr) {
-        p.lse[static_cast<int64_t>(hq) * p.T + w.r.t0 + tok] =
+        p.lse[static_cast<int64_t>(hq) * p.T + w.t0 + tok] =
             l_run == 0.0f ? -INFINITY : (m_run + fast_log2(l_run)) * kLn2;
       }
       tc_fence_before();
       mbar_arrive(bOEmpty + 8 * t);
+      __syncwarp();
+      if (lane == 0) unit_done(m);
     }
   }
 
