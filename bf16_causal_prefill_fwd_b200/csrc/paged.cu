@@ -406,6 +406,7 @@ int b200attn_paged_fwd(const void* q, size_t q_stride, const b200attn_paged_cach
   p.Hq = Hq;
   p.Hkv = cache->Hkv;
   p.G = G;
+  p.group = b200p::fast_div(G);
   p.num_pages = cache->num_pages;
   p.page_size = cache->page_size;
   p.max_q = max_seqlen_q;

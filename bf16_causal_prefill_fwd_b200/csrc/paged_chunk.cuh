@@ -303,6 +303,10 @@ __device__ __forceinline__ void ch_exp2_fma(float x0, float x1, float& r0, float
   r1 = x1 >= -125.0f ? __uint_as_float(__float_as_uint(p1) + (__float_as_uint(j1) << 23)) : 0.0f;
 }
 
+__device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+
 __device__ __forceinline__ __half2 bits_half2(uint32_t x) {
   __half2 h;
   memcpy(&h, &x, 4);
@@ -684,7 +688,7 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
       float c_log2 = p.scale_log2;
       int see, see_all, end;
       {
-      const int rtok = r / p.G, rhead = r - rtok * p.G;
+      const int rtok = r / p.G;
       const int tok = w.tok0 + t * tpt + rtok;
       const bool real = rtok < tpt && tok < w.nq;
       const bool whole = w.whole != 0, head = w.kb > 0;
@@ -710,50 +714,69 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
         continue;
       }
       if constexpr (FP8) {
-        // this row of Q as two e4m3 numbers per element, side by side: codes
-        // [0, d) nearest, [d, 2 d) the rest
-        constexpr int W = DQK / 2;
-        uint32_t q[W];
-        const uint4* src = reinterpret_cast<const uint4*>(
-            p.q + (w.t0 + (real ? tok : 0)) * p.q_stride + static_cast<int64_t>(w.h * p.G + (real ? rhead : 0)) * DQK);
-        float amax = 0.0f;
-#pragma unroll
-        for (int i = 0; i < W / 4; ++i) {
-          const uint4 x = real ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-          q[4 * i] = x.x, q[4 * i + 1] = x.y, q[4 * i + 2] = x.z, q[4 * i + 3] = x.w;
-        }
-#pragma unroll
-        for (int i = 0; i < W; ++i)
-          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(q[i] << 16)), fabsf(__uint_as_float(q[i] & 0xffff0000u))));
-        int e = 0;
-        if (amax > 0.0f && amax < INFINITY)
-          e = max(-118, min(126, static_cast<int>(__float_as_uint(amax) >> 23) - 134));
-        float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        if (amax == INFINITY) down = __uint_as_float(0x7fffffffu);  // an infinite element: NaN scores
-        c_log2 *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * __ldg(p.k_scale + w.h);
+        // Q as two e4m3 numbers per element, side by side: codes [0, d) nearest,
+        // [d, 2 d) the rest. Eight lanes take a row, so that loads are whole lines;
+        // a row's factor then goes to the thread that has its scores.
         if (units > 0) ok = paged_wait(bQEmpty + 8 * t, (units - 1) & 1, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint32_t row = sQ + t * C::Q_BYTES + r * 128;
+        constexpr int NU = DQK / 64;  // 16-byte pieces of a row per lane
+        const int l8 = lane & 7;
+        float mine = 1.0f;
+        uint4 rows[8][NU];  // every load under way before the first is used
 #pragma unroll
-        for (int i = 0; i < W / 8; ++i) {  // 16 elements
-          uint32_t hi[4], lo[4];
+        for (int s = 0; s < 8; ++s) {
+          const int rr = 32 * (warp & 3) + 4 * s + (lane >> 3);
+          const int rt = static_cast<uint32_t>(rr) / p.group, tk = w.tok0 + t * tpt + rt;
+          const bool has = rt < tpt && tk < w.nq;
+          const uint4* src = reinterpret_cast<const uint4*>(
+              p.q + (w.t0 + (has ? tk : 0)) * p.q_stride +
+              static_cast<int64_t>(w.h * p.G + (has ? rr - rt * p.G : 0)) * DQK) + l8;
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const uint32_t a = q[8 * i + 2 * n], b = q[8 * i + 2 * n + 1];
-            const float f0 = __uint_as_float(a << 16) * down, f1 = __uint_as_float(a & 0xffff0000u) * down;
-            const float f2 = __uint_as_float(b << 16) * down, f3 = __uint_as_float(b & 0xffff0000u) * down;
-            const uint32_t h01 = pack_e4m3x2(f0, f1), h23 = pack_e4m3x2(f2, f3);
-            const float2 g01 = __half22float2(bits_half2(e4m3x2_f16x2(h01)));
-            const float2 g23 = __half22float2(bits_half2(e4m3x2_f16x2(h23)));
-            hi[n] = h01 | (h23 << 16);
-            lo[n] = static_cast<uint32_t>(pack_e4m3x2(f0 - g01.x, f1 - g01.y)) |
-                    (static_cast<uint32_t>(pack_e4m3x2(f2 - g23.x, f3 - g23.y)) << 16);
-          }
-          const int uh = i, ul = DQK / 16 + i;  // 16-byte units of the row
-          st_shared_v4(row + (uh >> 3) * C::CHUNK + (((uh & 7) ^ (r & 7)) << 4), hi[0], hi[1], hi[2], hi[3]);
-          st_shared_v4(row + (ul >> 3) * C::CHUNK + (((ul & 7) ^ (r & 7)) << 4), lo[0], lo[1], lo[2], lo[3]);
+          for (int n = 0; n < NU; ++n) rows[s][n] = has ? __ldg(src + 8 * n) : make_uint4(0, 0, 0, 0);
         }
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          const int rr = 32 * (warp & 3) + 4 * s + (lane >> 3);
+          const uint4(&x)[NU] = rows[s];
+          float amax = 0.0f;
+          auto absmax2 = [](uint32_t v) {
+            return fmaxf(fabsf(__uint_as_float(v << 16)), fabsf(__uint_as_float(v & 0xffff0000u)));
+          };
+#pragma unroll
+          for (int n = 0; n < NU; ++n)
+            amax = fmaxf(amax, fmaxf(fmaxf(absmax2(x[n].x), absmax2(x[n].y)), fmaxf(absmax2(x[n].z), absmax2(x[n].w))));
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          int e = 0;
+          if (amax > 0.0f && amax < INFINITY)
+            e = max(-118, min(126, static_cast<int>(__float_as_uint(amax) >> 23) - 134));
+          float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          if (amax == INFINITY) down = __uint_as_float(0x7fffffffu);  // an infinite element: NaN scores
+          const float up = __shfl_sync(0xffffffffu, __uint_as_float(static_cast<uint32_t>(127 + e) << 23), 8 * (lane & 3));
+          if ((lane >> 2) == s) mine = up;
+          const uint32_t row = sQ + t * C::Q_BYTES + rr * 128;
+#pragma unroll
+          for (int n = 0; n < NU; ++n) {
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t a = k ? x[n].z : x[n].x, b = k ? x[n].w : x[n].y;
+              const float f0 = __uint_as_float(a << 16) * down, f1 = __uint_as_float(a & 0xffff0000u) * down;
+              const float f2 = __uint_as_float(b << 16) * down, f3 = __uint_as_float(b & 0xffff0000u) * down;
+              const uint32_t h01 = pack_e4m3x2(f0, f1), h23 = pack_e4m3x2(f2, f3);
+              const float2 g01 = __half22float2(bits_half2(e4m3x2_f16x2(h01)));
+              const float2 g23 = __half22float2(bits_half2(e4m3x2_f16x2(h23)));
+              hi[k] = h01 | (h23 << 16);
+              lo[k] = static_cast<uint32_t>(pack_e4m3x2(f0 - g01.x, f1 - g01.y)) |
+                      (static_cast<uint32_t>(pack_e4m3x2(f2 - g23.x, f3 - g23.y)) << 16);
+            }
+            const int uh = 4 * n + (l8 >> 1), ul = DQK / 16 + uh;  // 16-byte units of the row
+            st_shared_v2(row + (uh >> 3) * C::CHUNK + (((uh & 7) ^ (rr & 7)) << 4) + 8 * (l8 & 1), hi[0], hi[1]);
+            st_shared_v2(row + (ul >> 3) * C::CHUNK + (((ul & 7) ^ (rr & 7)) << 4) + 8 * (l8 & 1), lo[0], lo[1]);
+          }
+        }
+        c_log2 *= mine * __ldg(p.k_scale + w.h);
         fence_proxy_async_smem();
         mbar_arrive(bQFull + 8 * t);
       }

@@ -131,6 +131,7 @@ struct PagedAttn {
   const int* cu;       // [B + 1] first new token of each request
   const int* kv_lens;  // [B] keys of each request, new ones included
   int B, T, Hq, Hkv, G;
+  FastDiv group;  // G
   int num_pages, page_size;
   int box;       // rows of a page one TMA copy takes: gcd(page_size, key tile)
   int max_q;     // bound on the new tokens of one request
