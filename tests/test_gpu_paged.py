@@ -311,3 +311,266 @@ def test_strided_caches_and_slices_of_a_fused_projection():
         b2.paged_append_kv(k, v, a, c, slots)
         assert torch.equal(torch.nan_to_num(kc), torch.nan_to_num(a)) and torch.equal(torch.nan_to_num(vc), torch.nan_to_num(c))
     assert b2.check() == 0
+
+
+# ------------------------------------------------------------------------------------------- contents that do not fit
+
+@pytest.mark.parametrize("max_q", [1, None])
+def test_contents_that_do_not_fit_are_skipped_and_reported(max_q):
+    """A request whose lengths do not fit, or with more new tokens than announced, leaves its rows as they are; the
+    others are computed."""
+    n = 1 if max_q == 1 else 20
+    p = make([n] * 4, [50, 60, 70, 80], 8, 2, 128, 16, seed=21)
+    good = p.cuda()
+    want = b2.attn_paged_fwd(*good.args(), max_seqlen_q=max_q)
+    assert b2.check() == 0
+    for kv in (-1, 16 * p.table.shape[1] + 1):
+        bad = p.cuda()
+        bad.kv_lens[2] = kv
+        out = torch.full_like(want, 7.0)
+        b2.attn_paged_fwd(*bad.args(), max_seqlen_q=max_q, out=out)
+        assert b2.check() == -1
+        assert torch.equal(out[: 2 * n], want[: 2 * n]) and torch.equal(out[3 * n:], want[3 * n:])
+        assert bool((out[2 * n: 3 * n] == 7.0).all())
+    for cu in ([0, n, 2 * n, 99, 4 * n], [0, n, -5, 3 * n, 4 * n], [0, n, 2 * n, n, 4 * n]):
+        bad = p.cuda()
+        bad.cu.copy_(torch.tensor(cu, dtype=torch.int32))
+        out = torch.full_like(want, 7.0)
+        b2.attn_paged_fwd(*bad.args(), max_seqlen_q=max_q, out=out)
+        assert b2.check() == -1
+        assert torch.equal(out[:n], want[:n])
+    assert torch.equal(b2.attn_paged_fwd(*good.args(), max_seqlen_q=max_q), want) and b2.check() == 0
+
+
+@pytest.mark.parametrize("n,max_q", [(1, 1), (20, 20)])
+def test_table_entries_that_are_no_page_read_as_zeros(n, max_q):
+    p = make([n, n], [60, 90], 8, 2, 128, 16, seed=22)
+    for entry in (-1, p.k_cache.shape[0], 2 ** 31 - 1):
+        bad = p.cuda()
+        bad.table[1, 2] = entry
+        o = b2.attn_paged_fwd(*bad.args(), max_seqlen_q=max_q)
+        assert b2.check() == -1
+        zero = Paged(**{k: v if v is None else v.clone() for k, v in p.__dict__.items()})
+        zero.k_cache[zero.table[1, 2].long()] = 0
+        zero.v_cache[zero.table[1, 2].long()] = 0
+        check_attention(zero, o)
+
+
+def test_rows_behind_the_last_request_stay_as_they_are():
+    for n, max_q in ((1, 1), (33, 33)):
+        p = make([n, 0, n], [100, 5, 60], 8, 2, 128, 16, seed=23, pad_rows=9)
+        d = p.cuda()
+        out = torch.full((2 * n + 9, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+        b2.attn_paged_fwd(*d.args(), max_seqlen_q=max_q, out=out)
+        assert b2.check() == 0
+        check_attention(p, out)
+        assert bool((out[2 * n:] == 7.0).all())
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n,max_q", [(1, 1), (40, 40)])
+def test_nan_reaches_the_rows_that_see_it_and_no_other(n, max_q, e4m3):
+    p = make([n, n, n], [90, 200, 150], 8, 2, 128, 16, e4m3, seed=24)
+    ref = run(p, max_seqlen_q=max_q)
+    for cache in ("k_cache", "v_cache"):
+        bad = Paged(**{k: v if v is None else v.clone() for k, v in p.__dict__.items()})
+        page = int(bad.table[1, 1])
+        getattr(bad, cache).view(torch.uint8 if e4m3 else torch.int16)[page, 3, 1, 5] = 0x7F if e4m3 else 0x7FC0
+        o, lse = run(bad, max_seqlen_q=max_q)
+        hit = torch.zeros(3 * n, 8, dtype=torch.bool)
+        hit[n: 2 * n, 4:] = True  # key 19 of request 1, key/value head 1: seen by all its new tokens
+        nan = o.isnan().any(-1).cpu()
+        assert torch.equal(nan, hit)
+        assert torch.equal(o[~hit.cuda()], ref[0][~hit.cuda()])
+        if cache == "k_cache":
+            assert bool(lse.T.isnan().cpu()[hit].all())
+
+
+@pytest.mark.parametrize("n,max_q", [(1, 1), (40, 40)])
+def test_infinite_query_gives_nan_in_its_row_only(n, max_q):
+    for e4m3 in (False, True):
+        p = make([n, n], [90, 200], 8, 2, 128, 16, e4m3, seed=25)
+        ref = run(p, max_seqlen_q=max_q)[0]
+        p.q[n, 3, 7] = math.inf
+        o = run(p, max_seqlen_q=max_q)[0]
+        assert bool(o[n, 3].isnan().all())
+        rest = torch.ones(2 * n, 8, dtype=torch.bool)
+        rest[n, 3] = False
+        assert torch.equal(o[rest.cuda()], ref[rest.cuda()])
+
+
+# ------------------------------------------------------------------------------------------- sizes
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_many_short_requests(e4m3):
+    """More requests than a block has threads."""
+    B = 1300
+    kv = [1 + (i * 37) % 45 for i in range(B)]
+    p = make([i % 2 for i in range(B)], kv, 4, 2, 128, 16, e4m3, seed=26)
+    check_attention(p, *run(p, max_seqlen_q=1))
+    p = make([(i * 7) % 12 for i in range(B)], [n + 12 for n in kv], 4, 2, 128, 16, e4m3, seed=27)
+    check_attention(p, *run(p, max_seqlen_q=11))
+
+
+def test_decoding_and_chunk_kernels_agree():
+    """The same decoding step with and without a bound on the new tokens."""
+    p = make([1, 1, 1, 1], [1, 130, 64, 999], 32, 8, 128, 16, seed=28)
+    few, many = run(p, max_seqlen_q=1), run(p)
+    check_attention(p, *few)
+    check_attention(p, *many)
+
+
+def test_offsets_past_32_bits():
+    """A cache whose last pages begin past 2^32 bytes and 2^31 elements."""
+    pages, ps, H = 33000, 64, 8
+    kc, vc = (torch.empty(pages, ps, H, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    assert kc.numel() * 2 > 2 ** 32 and kc[:-3].numel() > 2 ** 31
+    q_lens, kv_lens = [1, 1], [100, 150]
+    p = make(q_lens, kv_lens, 32, H, 128, ps, seed=29)
+    n = p.k_cache.shape[0]
+    d = p.cuda()
+    table = torch.where(d.table >= 0, d.table + (pages - n), d.table)
+    slots = torch.arange((pages - n) * ps, pages * ps, dtype=torch.int32, device="cuda")
+    b2.paged_append_kv(d.k_cache.flatten(0, 1), d.v_cache.flatten(0, 1), kc, vc, slots)
+    for max_q in (1, None):
+        o = b2.attn_paged_fwd(d.q, kc, vc, table, d.cu, d.kv_lens, max_seqlen_q=max_q)
+        assert b2.check() == 0
+        check_attention(p, o)
+    del kc, vc
+
+
+# ------------------------------------------------------------------------------------------- as a server uses them
+
+def dense(q, k, v, n_ctx):
+    """64-bit causal attention of one request: q the last rows of a sequence of k, v."""
+    nq, G = q.shape[0], q.shape[1] // k.shape[1]
+    kk, vv = k.double().repeat_interleave(G, 1), v.double().repeat_interleave(G, 1)
+    x = torch.einsum("ihd,jhd->hij", q.double(), kk) / math.sqrt(q.shape[2])
+    x.masked_fill_(torch.arange(k.shape[0])[None, :] > n_ctx + torch.arange(nq)[:, None], -math.inf)
+    return torch.einsum("hij,jhd->ihd", torch.softmax(x, 2), vv)
+
+
+@pytest.mark.parametrize("d_qk,e4m3", [(128, False), (128, True), (192, False)])
+def test_serving_steps_together(d_qk, e4m3):
+    """Prompts read in chunks, decoding, requests of different ages in one step: lengths -> slots and pages -> K and V
+    appended -> attention, each step's output against dense attention of each request's whole history."""
+    Hq, H, ps, B = 8, 2, 16, 4
+    g = torch.Generator().manual_seed(d_qk + e4m3)
+    plan = [[30, 17, 1, 0], [30, 1, 1, 0], [1, 1, 1, 90], [1, 3, 0, 1], [1, 1, 1, 1]]
+    total = sum(sum(s) for s in plan)
+    pages = total // ps + 2 * B
+    dt = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    kc, vc = (torch.full((pages, ps, H, d), math.nan, device="cuda").to(dt) for d in (d_qk, 128))
+    scale = dict(k_scale=torch.full((H,), 0.011, device="cuda"), v_scale=torch.full((H,), 0.012, device="cuda")) if e4m3 else {}
+    table = torch.full((B, 12), -1, dtype=torch.int32, device="cuda")
+    free, head, ctx = torch.randperm(pages, generator=g).to(torch.int32).cuda(), ints([0]), ints([0] * B)
+    history = [(torch.empty(0, H, d_qk), torch.empty(0, H, 128)) for _ in range(B)]
+    for new in plan:
+        T, pad = sum(new), 3
+        q, k, v = (torch.randn(T + pad, h, d, generator=g).to(torch.bfloat16) for h, d in ((Hq, d_qk), (H, d_qk), (H, 128)))
+        cu, kv, pos, slots, head = b2.paged_slots(table, ctx, ints(new), T + pad, ps, free_pages=free, free_head=head)
+        o = b2.attn_paged_func(q.cuda(), k.cuda(), v.cuda(), kc, vc, table, cu, kv, slots, max_seqlen_q=max(new), **scale)
+        assert b2.check() == 0
+        t = 0
+        for b, n in enumerate(new):
+            stored = (k[t:t + n], v[t:t + n])
+            if e4m3:
+                stored = tuple(plain_codes(x, s.cpu()).float() * s.cpu()[:, None] for x, s in
+                               zip(stored, (scale["k_scale"], scale["v_scale"])))
+            old = history[b]
+            history[b] = tuple(torch.cat([a, x.float()]) for a, x in zip(old, stored))
+            if n:
+                want = dense(q[t:t + n], *history[b], old[0].shape[0])
+                spread = dense(q[t:t + n], history[b][0], history[b][1].abs(), old[0].shape[0])
+                # the bounds of check_attention for scores of this size (|q| |k| / sqrt(d) below 32)
+                lim = spread * (2.0 ** -8 + 2 * (d_qk * 32 * 2.0 ** -24 + 2.3e-4)) + want.abs() * 2.0 ** -8
+                assert bool(((o[t:t + n].double().cpu() - want).abs() <= lim).all())
+            t += n
+        ctx = kv
+    assert int(head) == sum(-(-sum(s[b] for s in plan) // ps) for b in range(B))
+
+
+@pytest.mark.parametrize("max_q", [1, 24])
+def test_captured_steps_replay_on_new_contents(max_q):
+    """A padded step captured once -- slots, append, attention -- and replayed with other lengths, tables and values;
+    two graphs with workspaces of their own replayed in turn."""
+    Hq, H, d, ps, B, T = 8, 2, 128, 16, 5, 5 * max_q
+    g = torch.Generator().manual_seed(max_q)
+    pages, width = 80, 12
+    mk = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda")
+    kc, vc = (torch.randn(pages, ps, H, d, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    q, k, v = mk(T, Hq, d), mk(T, H, d), mk(T, H, d)
+    table, ctx, new = torch.zeros(B, width, dtype=torch.int32, device="cuda"), ints([1] * B), ints([1] * B)
+    q.zero_(), k.zero_(), v.zero_()
+    graphs = []
+    for _ in range(2):
+        out = torch.full((T, Hq, d), 7.0, dtype=torch.bfloat16, device="cuda")
+        ws = torch.empty(b2.attn_paged_workspace_bytes(T, max_q, Hq, H), dtype=torch.uint8, device="cuda")
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            def step():
+                cu, kv, pos, slots = b2.paged_slots(table, ctx, new, T, ps)
+                b2.paged_append_kv(k, v, kc, vc, slots)
+                b2.attn_paged_fwd(q, kc, vc, table, cu, kv, max_seqlen_q=max_q, out=out, workspace=ws)
+                return cu, kv
+            step()
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            cu, kv = step()
+        graphs.append((graph, out, cu, kv, ws))  # a captured call's buffers live as long as its graph
+    for i in range(4):
+        n_new = [min(max_q, (i + b) % (max_q + 1)) for b in range(B)]
+        n_ctx = [(17 * (b + 1) * (i + 2)) % 150 for b in range(B)]
+        order = torch.randperm(pages, generator=g)[: B * width].view(B, width).to(torch.int32)
+        table.copy_(order)
+        ctx.copy_(torch.tensor(n_ctx)), new.copy_(torch.tensor(n_new))
+        for x in (q, k, v):
+            x.copy_(torch.randn(*x.shape, generator=g).to(torch.bfloat16))
+        graph, out, cu, kv, _ = graphs[i % 2]
+        out.fill_(7.0)
+        graph.replay()
+        assert b2.check() == 0
+        assert kv.tolist() == [a + c for a, c in zip(n_ctx, n_new)]
+        p = Paged(q.cpu(), kc.cpu(), vc.cpu(), table.cpu(), cu.cpu(), kv.cpu(), None, None)
+        check_attention(p, out)
+        assert bool((out[sum(n_new):] == 7.0).all())
+    for graph, *_ in graphs:
+        graph.reset()
+
+
+@pytest.mark.parametrize("n,max_q", [(1, 1), (40, 40)])
+def test_other_streams_and_repeated_calls_give_the_same_bytes(n, max_q):
+    p = make([n] * 6, [700 + 31 * i for i in range(6)], 32, 8, 128, 16, seed=30).cuda()
+    ref = b2.attn_paged_fwd(*p.args(), max_seqlen_q=max_q, return_lse=True)
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream() for _ in range(3)]
+    outs = []
+    for s in side * 3:  # overlapping calls, each with a workspace and an output of its own
+        with torch.cuda.stream(s):
+            outs.append(b2.attn_paged_fwd(*p.args(), max_seqlen_q=max_q, return_lse=True))
+    outs.append(b2.attn_paged_fwd(*p.args(), max_seqlen_q=max_q, return_lse=True, stream=side[0]))
+    torch.cuda.synchronize()
+    for o, lse in outs:
+        assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
+    assert b2.check() == 0
+
+
+def test_calls_do_not_wait_for_the_stream():
+    p = make([1, 1], [100, 60], 8, 2, 128, 16, seed=31).cuda()
+    k = torch.zeros(2, 2, 128, dtype=torch.bfloat16, device="cuda")
+    args = ints([99, 59]), ints([1, 1])
+    b2.paged_slots(p.table, *args, 2, 16)
+    slots = ints([-1, -1])
+    b2.attn_paged_func(p.q, k, k, p.k_cache, p.v_cache, p.table, p.cu, p.kv_lens, slots, max_seqlen_q=1)
+    b2.attn_paged_fwd(*p.args())
+    torch.cuda.synchronize()
+    busy = torch.cuda.Event()
+    torch.cuda._sleep(1_000_000_000)
+    busy.record()
+    b2.paged_slots(p.table, *args, 2, 16)
+    b2.attn_paged_func(p.q, k, k, p.k_cache, p.v_cache, p.table, p.cu, p.kv_lens, slots, max_seqlen_q=1)
+    b2.attn_paged_fwd(*p.args())
+    assert not busy.query()
+    assert b2.check() == 0
