@@ -1,10 +1,12 @@
-"""Build libb200attn.so in-tree with nvcc for sm_100a.
+"""Build libb200attn.so in-tree with nvcc for sm_100a, and _paged_binding.so.
 
     python -m bf16_causal_prefill_fwd_b200.build [--force] [--verbose] [--trace]
 
 The library is two translation units (csrc/b200attn.cu and csrc/paged.cu),
 compiled side by side, with the CUDA runtime linked statically, so it loads
-next to any PyTorch build.
+next to any PyTorch build. _paged_binding.so (csrc/paged_binding.cpp) is the
+compiled part of the paged-cache operators' Python binding, built against the
+installed PyTorch; it calls the library and holds no kernels.
 """
 from __future__ import annotations
 
@@ -21,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libb200attn.so")
 TRACE_LIB_PATH = os.path.join(LIB_DIR, "libb200attn_trace.so")  # same library with -DATTN_TRACE
+BINDING_PATH = os.path.join(LIB_DIR, "_paged_binding.so")
 HEADER = os.path.join(ROOT, "include", "b200attn.h")
 
 NVCC_FLAGS = [
@@ -51,10 +54,41 @@ def up_to_date(path: str = LIB_PATH) -> bool:
     return all(os.path.getmtime(s) <= t for s in sources())
 
 
+def _binding_cmd(out: str) -> list[str]:
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    return [shutil.which("g++") or "g++", "-O2", "-std=c++20", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + os.path.join(root, "include"),
+            "-I" + os.path.join(root, "include", "torch", "csrc", "api", "include"), "-I" + cuda,
+            "-I" + sysconfig.get_paths()["include"], os.path.join(CSRC, "paged_binding.cpp"), "-o", out,
+            "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
+
+
+def build_binding(force: bool = False) -> str:
+    """Build lib/_paged_binding.so."""
+    src = [os.path.join(CSRC, "paged_binding.cpp"), HEADER]
+    if not force and os.path.exists(BINDING_PATH) and all(
+            os.path.getmtime(s) <= os.path.getmtime(BINDING_PATH) for s in src):
+        return BINDING_PATH
+    os.makedirs(LIB_DIR, exist_ok=True)
+    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    res = subprocess.run(_binding_cmd(tmp), capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError("g++ failed building _paged_binding.so")
+    os.replace(tmp, BINDING_PATH)
+    return BINDING_PATH
+
+
 def build(force: bool = False, verbose: bool = False, trace: bool = False) -> str:
     """Build lib/libb200attn.so, or with trace=True lib/libb200attn_trace.so (the
     kernels record per-block events for b200attn_trace_read)."""
     path = TRACE_LIB_PATH if trace else LIB_PATH
+    build_binding(force)
     if not force and up_to_date(path):
         return path
     os.makedirs(LIB_DIR, exist_ok=True)

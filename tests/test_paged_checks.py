@@ -1,8 +1,10 @@
 """Argument checks of the paged-cache operators, on the host: what the binding
-refuses before the library is called (the library replaced by a stub that
-launches nothing, so these tests run on CPU tensors and reach no GPU), and what
+refuses before the library is called (the library's functions replaced by
+stand-ins that launch nothing, so these tests run on CPU tensors and reach no
+GPU), and what
 the C entry points refuse before they touch a device."""
 import ctypes
+import struct
 
 import pytest
 import torch
@@ -13,31 +15,45 @@ from bf16_causal_prefill_fwd_b200 import _paged as p
 E4M3 = torch.float8_e4m3fn
 
 
-class StubLib:
+class Stub:
+    """Stands for the library: records the calls, launches nothing."""
+
     def __init__(self):
         self.calls = []
+        i, vp, sz, f = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
+        types = {"slots": [vp, sz, i, vp, vp, i, i, i, vp, i] + [vp] * 7, "append": [vp, vp, sz, sz, i, vp, vp, vp],
+                 "fwd": [vp, sz, vp, vp, sz, i, vp, vp, i, i, i, i, i, f, vp, vp, vp, sz, vp]}
+        self.fns = [ctypes.CFUNCTYPE(i, *t)(self._record(n)) for n, t in types.items()]
+        self.fns.append(ctypes.CFUNCTYPE(sz, i, i, i, i)(lambda *a: 64))
+        self.addresses = [ctypes.cast(x, ctypes.c_void_p).value for x in self.fns]
 
-    def __getattr__(self, name):
-        if name.endswith("_workspace_bytes"):
-            return lambda *args: 64
-        if name == "b200attn_strerror":
-            return lambda code: b"stub"
-        if name.startswith("b200attn_"):
-            return lambda *args: self.calls.append((name, args)) or 0
-        raise AttributeError(name)
+    def _record(self, name):
+        def fn(*args):
+            cache = {"append": 5, "fwd": 2}.get(name)
+            args = list(args)
+            if cache is not None:
+                args[cache] = CACHE.unpack(ctypes.string_at(args[cache], CACHE.size))
+            self.calls.append((name, args))
+            return 0
+        return fn
+
+
+@pytest.fixture(scope="module")
+def real():
+    from bf16_causal_prefill_fwd_b200 import build
+    build.build()
+    return b.load_library()
 
 
 @pytest.fixture
-def lib(monkeypatch):
-    stub = StubLib()
-    monkeypatch.setattr(b, "load_library", lambda path=None: stub)
-    monkeypatch.setattr(b, "_lib", stub)
-    monkeypatch.setattr(b, "_check_cuda_contig", lambda name, t: None)
-    monkeypatch.setattr(p, "_device_of", lambda t: 0 if isinstance(t, torch.Tensor) else t.get_device())
-    monkeypatch.setattr(p, "_current_device", lambda: 0)
-    return stub
+def lib(real):
+    stub, native = Stub(), p._load()
+    native.bind(*stub.addresses, True)
+    yield stub
+    p._bind(native)
 
 
+CACHE = struct.Struct("@2P6q6i2P")  # b200attn_paged_cache
 P, PS, HQ, HKV, D, T, B, W = 6, 16, 8, 2, 128, 5, 3, 4
 
 
@@ -95,8 +111,8 @@ def test_views_the_kernels_take_as_they_are(lib):
     attn(lib, q=q, kc=hnd, vc=both[:, 1], table=ints(B, 9)[:, :W])
     append(lib, k=k, v=v, kc=both[:, 0], vc=both[:, 1])
     name, args = lib.calls[0]
-    assert args[1] == qkv.stride(0) and args[4] == 9 and args[5] == W
-    strides = p._CACHE.unpack(args[2])[2:8]
+    assert name == "fwd" and args[1] == qkv.stride(0) and args[4] == 9 and args[5] == W
+    strides = args[2][2:8]
     assert strides == (PS * HKV * D, D, PS * D, 2 * PS * HKV * D, HKV * D, D)
 
 
@@ -146,13 +162,21 @@ def test_slots_refuses(lib, bad):
     assert lib.calls == []
 
 
-def test_cpu_tensors_are_refused():
+def test_cpu_tensors_are_refused(real):
+    for call in (attn, append, slots):
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            call(None)
+
+
+def test_arguments_of_other_kinds_are_refused(lib):
+    for bad in (dict(q="x"), dict(kc=None, k_scale="x"), dict(max_seqlen_q=1.5), dict(max_seqlen_q=2 ** 70)):
+        with pytest.raises(ValueError):
+            attn(lib, **bad)
+    with pytest.raises(TypeError):
+        attn(lib, softmax_scale="x")
     with pytest.raises(ValueError):
-        attn(None)
-    with pytest.raises(ValueError):
-        append(None)
-    with pytest.raises(ValueError):
-        slots(None)
+        slots(lib, total=2.5)
+    assert lib.calls == []
 
 
 # ------------------------------------------------------------------------------------------- C entry points
@@ -160,15 +184,8 @@ def test_cpu_tensors_are_refused():
 FAKE = 0x10000  # 16-byte aligned, never dereferenced
 
 
-@pytest.fixture(scope="module")
-def real():
-    from bf16_causal_prefill_fwd_b200 import build
-    build.build()
-    return b.load_library()
-
-
 def cache(k=FAKE, v=FAKE, page=PS * HKV * D, token=HKV * D, head=D, pages=P, ps=PS, h=HKV, dqk=D, dv=D, dtype=0, ks=0, vs=0):
-    return p._CACHE.pack(k, v, page, token, head, page, token, head, pages, ps, h, dqk, dv, dtype, ks, vs)
+    return CACHE.pack(k, v, page, token, head, page, token, head, pages, ps, h, dqk, dv, dtype, ks, vs)
 
 
 def c_attn(lib, c, q=FAKE, stride=HQ * D, table=FAKE, row=W, width=W, cu=FAKE, kv=FAKE, batch=B, total=T, maxq=T, hq=HQ,
