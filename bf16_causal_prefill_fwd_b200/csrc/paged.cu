@@ -145,19 +145,26 @@ bool page_maps(CUtensorMap* tk, CUtensorMap* tv, const b200attn_paged_cache* c, 
                   c->v_page_stride, rows, swizzle_v);
 }
 
-// Launch whose blocks may be scheduled while the kernel before it drains (that
-// kernel and this one contain the matching griddepcontrol instructions).
+// Launch whose blocks may be scheduled while the kernel before it in the stream
+// drains. Every kernel of this file first waits for that kernel and its writes
+// (griddepcontrol.wait), so only the launch itself and the block's set-up
+// overlap; each lets its successor do the same once all its blocks run.
 template <typename... Args>
-int launch_dependent(void (*kern)(Args...), dim3 grid, int threads, cudaStream_t st, Args... args) {
+int launch(void (*kern)(Args...), dim3 grid, int threads, int smem, int cluster, cudaStream_t st, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? B200ATTN_OK : B200ATTN_ERR_CUDA;
 }
 
@@ -192,10 +199,10 @@ int launch_decode(const b200attn_paged_cache* c, PagedAttn p, int sm_count, int 
   if (rc != B200ATTN_OK) return rc;
   int blocks = C::BLOCKS * sm_count;
   if (blocks > b200p::kDecMaxBlocks) blocks = b200p::kDecMaxBlocks;
-  kern<<<blocks, b200p::kDecThreads, C::SMEM, st>>>(tk, tv, p);
-  if (cudaGetLastError() != cudaSuccess) return B200ATTN_ERR_CUDA;
-  return launch_dependent(b200p::paged_join_kernel<128>, dim3(blocks, 4, 1), 128, st,
-                          static_cast<const PagedAttn>(p));
+  const int lrc = launch(kern, dim3(blocks, 1, 1), b200p::kDecThreads, C::SMEM, 1, st, static_cast<const CUtensorMap>(tk),
+                         static_cast<const CUtensorMap>(tv), static_cast<const PagedAttn>(p));
+  if (lrc != B200ATTN_OK) return lrc;
+  return launch(b200p::paged_join_kernel<128>, dim3(blocks, 4, 1), 128, 0, 1, st, static_cast<const PagedAttn>(p));
 }
 
 template <int DQK, bool FP8>
@@ -234,9 +241,12 @@ int launch_chunk(const b200attn_paged_cache* c, PagedAttn p, int sm_count, int d
   const int rc = prepare_kernel(reinterpret_cast<const void*>(kern), C::SMEM, C::REGS_LAUNCH, device, done);
   if (rc != B200ATTN_OK) return rc;
   const int blocks = sm_count < b200p::kChMaxBlocks ? sm_count : b200p::kChMaxBlocks;
-  kern<<<blocks, C::THREADS, C::SMEM, st>>>(tq, tk, tv, p);
-  if (cudaGetLastError() != cudaSuccess) return B200ATTN_ERR_CUDA;
-  return launch_dependent(b200p::paged_join_kernel<128>, dim3(blocks, p.slot_rows < 16 ? 4 : 16, 1), 128, st, static_cast<const PagedAttn>(p));
+  const int lrc = launch(kern, dim3(blocks, 1, 1), C::THREADS, C::SMEM, 1, st, static_cast<const CUtensorMap>(tq),
+                         static_cast<const CUtensorMap>(tk), static_cast<const CUtensorMap>(tv),
+                         static_cast<const PagedAttn>(p));
+  if (lrc != B200ATTN_OK) return lrc;
+  return launch(b200p::paged_join_kernel<128>, dim3(blocks, p.slot_rows < 16 ? 4 : 16, 1), 128, 0, 1, st,
+                static_cast<const PagedAttn>(p));
 }
 
 }  // namespace
@@ -295,21 +305,8 @@ int b200attn_paged_slots(int* block_table, size_t table_stride, int table_width,
   // One cluster: its barrier stands between reading the free list's head and
   // writing it. A step that one block covers in a pass or two takes one block.
   const int blocks = total <= b200p::kSlotsThreads ? 1 : b200p::kSlotsCluster;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, 1, 1);
-  cfg.blockDim = dim3(b200p::kSlotsThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = blocks;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, b200p::paged_slots_kernel, static_cast<const b200p::PagedSlots>(p)) == cudaSuccess
-             ? B200ATTN_OK
-             : B200ATTN_ERR_CUDA;
+  return launch(b200p::paged_slots_kernel, dim3(blocks, 1, 1), b200p::kSlotsThreads, smem, blocks,
+                static_cast<cudaStream_t>(stream), static_cast<const b200p::PagedSlots>(p));
 }
 
 int b200attn_paged_append(const void* k, const void* v, size_t k_stride, size_t v_stride, int total,
@@ -354,8 +351,7 @@ int b200attn_paged_append(const void* k, const void* v, size_t k_stride, size_t 
   auto kern = cache->dtype == B200ATTN_BF16
                   ? (cache->d_qk == 128 ? b200p::paged_append_kernel<128, 128, false> : b200p::paged_append_kernel<192, 128, false>)
                   : (cache->d_qk == 128 ? b200p::paged_append_kernel<128, 128, true> : b200p::paged_append_kernel<192, 128, true>);
-  kern<<<blocks, b200p::kAppendThreads, 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? B200ATTN_OK : B200ATTN_ERR_CUDA;
+  return launch(kern, dim3(blocks, 1, 1), b200p::kAppendThreads, 0, 1, st, static_cast<const b200p::PagedAppend>(p));
 }
 
 size_t b200attn_paged_fwd_workspace_bytes(int total, int max_seqlen_q, int Hq, int Hkv) {

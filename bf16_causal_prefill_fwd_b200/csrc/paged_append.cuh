@@ -61,6 +61,8 @@ struct CodeScale {
 template <int DQK, int DV, bool FP8>
 __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const PagedAppend p) {
   constexpr int UK = DQK / kAppendUnit, UV = DV / kAppendUnit;
+  pdl_launch_dependents();
+  pdl_wait();
   const uint32_t k_units = p.H * UK;
   const uint32_t n = p.T * p.per_token.d;  // < 2^31 (the host checks)
   for (uint32_t i = blockIdx.x * kAppendThreads + threadIdx.x; i < n; i += gridDim.x * kAppendThreads) {

@@ -431,6 +431,7 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
     tmem_relinquish();
   }
   ChStart* start = reinterpret_cast<ChStart*>(bar_gen + 8 * C::BARS + 8);
+  pdl_wait();
   const ChStart d = ch_start<C::THREADS>(p, tpt, reinterpret_cast<int*>(gen));  // in the Q buffers, not in use yet
   if (threadIdx.x == 0) *start = d;
   fence_proxy_async_smem();  // TMA writes there next

@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<DQK, DV, FP8, NT>::BLOCKS)
   const uint32_t bFull = s_bar, bEmpty = s_bar + 8 * C::STAGES;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  pdl_launch_dependents();  // the joining kernel's blocks may come in as this grid's leave
+  pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(bFull + 8 * s, 1);
@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<DQK, DV, FP8, NT>::BLOCKS)
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
   }
+  pdl_wait();
   const DecStart d = dec_start(p, s_plan);  // its barriers order the set-up above too
   __syncthreads();
   if (threadIdx.x == 0) reinterpret_cast<PartDesc*>(p.desc)[blockIdx.x].last = -1;
@@ -559,6 +560,7 @@ template <int DV>
 __global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttn p) {
   static_assert(DV == 128, "8 lanes x 16 or 32 lanes x 4 columns");
   __shared__ float s_o[4][DV], s_ml[4][2];
+  pdl_launch_dependents();
   pdl_wait();
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const PartDesc e = reinterpret_cast<const PartDesc*>(p.desc)[c];

@@ -71,6 +71,8 @@ __global__ void __launch_bounds__(kSlotsThreads) paged_slots_kernel(const PagedS
   const int ps = p.page_size;
   const bool alloc = p.free_pages != nullptr;
   if (tid == 0) s_bad = 0;
+  pdl_launch_dependents();
+  pdl_wait();
   __syncthreads();
 
   const int head = alloc ? *p.head_in : 0;
