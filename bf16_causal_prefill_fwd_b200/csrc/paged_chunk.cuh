@@ -63,19 +63,19 @@ struct ChCfg {
   static constexpr int THREADS = 384, REGS_LAUNCH = 168;
   // Register split by warpgroup: copies and issue, softmax; the sum stays within
   // what the block was launched with.
-  static constexpr int REGS_CTRL = FP8 ? 80 : 72, REGS_SOFT = FP8 ? 200 : 208;
+  static constexpr int REGS_CTRL = FP8 ? (DQK == 128 ? 80 : 104) : 72, REGS_SOFT = FP8 ? 200 : 208;
   static_assert(128 * REGS_CTRL + 256 * REGS_SOFT <= THREADS * REGS_LAUNCH, "registers");
   static constexpr int CHUNK = kChM * 128;  // 128 rows x 128 bytes, swizzled
   static constexpr int KSZ = FP8 ? 1 : 2;
   static constexpr int Q_CHUNKS = 2 * DQK / 128;  // bf16, or two halves of codes side by side
   static constexpr int K_CHUNKS = (DQK * KSZ + 127) / 128, V_CHUNKS = DV / 64;
   static constexpr int Q_BYTES = Q_CHUNKS * CHUNK, K_BYTES = K_CHUNKS * CHUNK, V_BYTES = V_CHUNKS * CHUNK;
-  static constexpr int STAGES = FP8 ? 2 : 0, VC_BYTES = kChN * DV;  // staged codes of V
+  static constexpr int STAGES = FP8 ? (DQK == 128 ? 3 : 2) : 0, VC_BYTES = kChN * DV;  // staged codes of V
   static constexpr int AVAIL = 227 * 1024 - 2048 - 2 * Q_BYTES - STAGES * VC_BYTES;
   static constexpr int PAIRS = AVAIL / (K_BYTES + V_BYTES);
   static constexpr int SV = PAIRS >= 2 ? 2 : 1;
   static constexpr int SK_FIT = (AVAIL - SV * V_BYTES) / K_BYTES, SK = SK_FIT > 4 ? 4 : SK_FIT;
-  static constexpr int BARS = 2 + 2 + 2 * SK + 2 * SV + 1 + 4 + 2 + 1 + 2 + 2 + 2 + 2 + 2 + 2 * kChUnits;
+  static constexpr int BARS = 2 + 2 + 2 * SK + 2 * SV + 1 + 6 + 2 + 1 + 2 + 2 + 2 + 2 + 2 + 2 * kChUnits;
   static constexpr int SMEM = 2 * Q_BYTES + SK * K_BYTES + SV * V_BYTES + STAGES * VC_BYTES + 1024 + 1024;
   static_assert(8 * BARS + 8 + 32 <= 512 && 512 + kChUnits * 64 <= 1024 && SMEM <= 227 * 1024 && SK >= 2, "shared memory");
   // Tensor memory: S [0, 128) for both tiles in turn, O_t at 128 + 128 t, P_t
@@ -375,9 +375,9 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
   const uint32_t bVFull = bKEmpty + 8 * C::SK;   // [SV]
   const uint32_t bVEmpty = bVFull + 8 * C::SV;   // [SV]
   const uint32_t bVTail = bVEmpty + 8 * C::SV;   // a V block whose last rows must be cleared
-  const uint32_t bCFull = bVTail + 8;            // [2] staged codes of V (e4m3)
-  const uint32_t bCEmpty = bCFull + 16;          // [2] converted
-  const uint32_t bSFull = bCEmpty + 16;          // [2]
+  const uint32_t bCFull = bVTail + 8;            // [STAGES] staged codes of V (e4m3)
+  const uint32_t bCEmpty = bCFull + 24;          // [STAGES] converted
+  const uint32_t bSFull = bCEmpty + 24;          // [2]
   const uint32_t bSFree = bSFull + 16;           // [1] the S buffer has been copied out
   const uint32_t bPFull = bSFree + 8;            // [2]
   const uint32_t bPDone = bPFull + 16;           // [2]
@@ -403,12 +403,15 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
         mbar_init(bOFull + 8 * t, 1);
         mbar_init(bOEmpty + 8 * t, 128);
         mbar_init(bDrain + 8 * t, 1);
-        mbar_init(bCFull + 8 * t, 1);
-        mbar_init(bCEmpty + 8 * t, 64);
+        
       }
       for (int i = 0; i < kChUnits; ++i) {
         mbar_init(bUFull + 8 * i, 1);
         mbar_init(bUEmpty + 8 * i, FP8 ? 12 : 11);  // the warps that read units
+      }
+      for (int i = 0; i < C::STAGES; ++i) {
+        mbar_init(bCFull + 8 * i, 1);
+        mbar_init(bCEmpty + 8 * i, 64);
       }
       mbar_init(bSFree, 128);
       mbar_init(bVTail, 1);
@@ -426,12 +429,14 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
       prefetch_tmap(&tmK);
       prefetch_tmap(&tmV);
     }
+  }
+  ChStart* start = reinterpret_cast<ChStart*>(bar_gen + 8 * C::BARS + 8);
+  pdl_wait();
+  if (warp == 0) {  // not before: the kernel that is waited for may still need tensor memory
     __syncwarp();
     tmem_alloc(smem_addr(tmem_slot), 512);
     tmem_relinquish();
   }
-  ChStart* start = reinterpret_cast<ChStart*>(bar_gen + 8 * C::BARS + 8);
-  pdl_wait();
   const ChStart d = ch_start<C::THREADS>(p, tpt, reinterpret_cast<int*>(gen));  // in the Q buffers, not in use yet
   if (threadIdx.x == 0) *start = d;
   fence_proxy_async_smem();  // TMA writes there next
