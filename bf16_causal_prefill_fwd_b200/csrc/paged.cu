@@ -405,6 +405,7 @@ int b200attn_paged_fwd(const void* q, size_t q_stride, const b200attn_paged_cach
   p.group = b200p::fast_div(G);
   p.num_pages = cache->num_pages;
   p.page_size = cache->page_size;
+  p.rows = b200p::fast_div(cache->page_size);
   p.max_q = max_seqlen_q;
   p.causal = causal;
   const double s = softmax_scale > 0.0f ? static_cast<double>(softmax_scale)

@@ -475,20 +475,24 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
       bool ok = true;
       // Block j of request b's head h into slot s; `bar` counts its bytes. `kb`: the piece's first block.
       auto copy_block = [&](int b, int h, int kv, int kb, int j, uint32_t s, uint32_t bar) {
-        const int a = (j - kb) % ahead;
+        const int a = (j - kb) & (ahead - 1);  // 32 / boxes is a power of two
         if (a == 0) page = lane < ahead * boxes ? paged_page(p, b, j * kChN + lane * p.box, kv) : 0;
         if (lane == 0) mbar_arrive_expect_tx(bar, slot_bytes);
         __syncwarp();
         const int pg = __shfl_sync(0xffffffffu, page, a * boxes + (lane < issues ? box : 0));
         if (lane < issues)
           tma_load_4d(ring + s * slot_bytes + c * C::CHUNK + box * p.box * 128, tm, bar, c * (128 / C::KSZ), h,
-                      (j * kChN + box * p.box) % p.page_size, pg);
+                      paged_row(p, j * kChN + box * p.box), pg);
       };
-      // Slot of the it-th block, once the block before in it has been used.
-      auto slot_of = [&](uint32_t it) -> uint32_t {
-        const uint32_t s = it % nslot;
-        if (it >= nslot) ok = __all_sync(0xffffffffu, paged_wait(bEmpty + 8 * s, ((it / nslot) - 1) & 1, abort_flag));
-        return s;
+      // The ring's next slot, once the block before in it has been used.
+      uint32_t slot = nslot - 1, turns = ~0u;  // turns of the ring before this one
+      auto next_slot = [&]() -> uint32_t {
+        if (++slot == nslot) {
+          slot = 0;
+          ++turns;
+        }
+        if (turns > 0) ok = __all_sync(0xffffffffu, paged_wait(bEmpty + 8 * slot, (turns - 1) & 1, abort_flag));
+        return slot;
       };
       // Tells the other roles the m-th unit (K warp).
       auto publish = [&](const ChWalk& w, uint32_t m) {
@@ -504,14 +508,14 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
         }
       };
       if constexpr (!FP8) {
-        uint32_t it = 0, m = 0;
+        uint32_t m = 0;
         if (is_k) {
           ChWalk w(p, start, tpt);
           for (;; w.next(), ++m) {
             publish(w, m);
             if (!ok || !w.valid()) break;
-            for (int j = w.kb; j < w.ke && ok; ++j, ++it) {
-              const uint32_t s = slot_of(it);
+            for (int j = w.kb; j < w.ke && ok; ++j) {
+              const uint32_t s = next_slot();
               if (ok) copy_block(w.b, w.h, w.r.kv, w.kb, j, s, bFull + 8 * s);
             }
           }
@@ -521,8 +525,8 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
           for (; ok; ++m) {
             ok = __all_sync(0xffffffffu, unit_get(m, w));
             if (!ok || !w.valid()) break;
-            for (int j = w.kb; j < w.ke && ok; ++j, ++it) {
-              const uint32_t s = slot_of(it);
+            for (int j = w.kb; j < w.ke && ok; ++j) {
+              const uint32_t s = next_slot();
               if (!ok) break;
               const bool tail = (j + 1) * kChN > w.kv;
               copy_block(w.b, w.h, w.kv, w.kb, j, s, tail ? bVTail : bFull + 8 * s);
@@ -570,7 +574,7 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
           if (!ok || !w.valid()) break;
           for (int j = w.kb; j < w.ke && ok; ++j, ++it) {
             for (; more && issued < it + nslot; ++issued) {
-              const uint32_t s = slot_of(issued);
+              const uint32_t s = next_slot();
               if (!ok) break;
               copy_block(ld.b, ld.h, ld.kv, ld.kb, lj, s, bFull + 8 * s);
               if (++lj >= ld.ke) ld_unit();

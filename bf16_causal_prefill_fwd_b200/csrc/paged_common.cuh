@@ -133,6 +133,7 @@ struct PagedAttn {
   int B, T, Hq, Hkv, G;
   FastDiv group;  // G
   int num_pages, page_size;
+  FastDiv rows;  // page_size
   int box;       // rows of a page one TMA copy takes: gcd(page_size, key tile)
   int max_q;     // bound on the new tokens of one request
   int causal;
@@ -173,12 +174,17 @@ __device__ __forceinline__ Request paged_request(const PagedAttn& p, int b, bool
 // the copy reads zeros) behind the last key and for a page number that is none.
 __device__ __forceinline__ int paged_page(const PagedAttn& p, int b, int key, int kv) {
   if (key >= kv) return p.num_pages;
-  const int page = __ldg(p.table + static_cast<int64_t>(b) * p.table_stride + key / p.page_size);
+  const int page = __ldg(p.table + static_cast<int64_t>(b) * p.table_stride + static_cast<uint32_t>(key) / p.rows);
   if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) {
     paged_report(kPagedInvalid);
     return p.num_pages;
   }
   return page;
+}
+
+// Row of its page that key `key` has.
+__device__ __forceinline__ int paged_row(const PagedAttn& p, int key) {
+  return key - static_cast<int>(static_cast<uint32_t>(key) / p.rows) * p.page_size;
 }
 
 // The part of a split unit that begins in a block, for the merge: its rows, and

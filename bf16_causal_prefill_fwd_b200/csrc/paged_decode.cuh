@@ -213,13 +213,13 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<DQK, DV, FP8, NT>::BLOCKS)
     // ------------------------------------------------------------ copies
     const int boxes = kDecKeys / p.box;  // per tile
     const int issues = boxes * (C::KC + C::VC);
-    const int ahead = 32 / boxes;        // tiles whose page numbers one load of the warp covers
+    const int ahead = 32 / boxes;        // tiles whose page numbers one load of the warp covers: a power of two
     uint32_t it = 0;
     bool ok = true;
     for (DecWalk w(p, d); ok && w.valid(); w.next()) {
       int page = 0;
       for (int k = 0; k < w.n; ++k, ++it) {
-        const int kt = w.k0 + k, a = k % ahead;
+        const int kt = w.k0 + k, a = k & (ahead - 1);
         if (a == 0) page = lane < ahead * boxes ? paged_page(p, w.b, kt * kDecKeys + lane * p.box, w.r.kv) : 0;
         const uint32_t s = it % C::STAGES;
         if (it >= C::STAGES) {
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<DQK, DV, FP8, NT>::BLOCKS)
         const int box = lane / (C::KC + C::VC), c = lane % (C::KC + C::VC);
         const int pg = __shfl_sync(0xffffffffu, page, a * boxes + (lane < issues ? box : 0));
         if (lane < issues) {
-          const int row = (kt * kDecKeys + box * p.box) % p.page_size;
+          const int row = paged_row(p, kt * kDecKeys + box * p.box);
           const uint32_t dst = base + s * C::STAGE + c * C::CHUNK + box * p.box * 128;
           if (c < C::KC)
             tma_load_4d(dst, &tmK, bFull + 8 * s, c * (128 / C::ESZ), w.h, row, pg);
