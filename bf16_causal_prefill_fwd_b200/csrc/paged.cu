@@ -189,7 +189,7 @@ bool few_rows(int max_q, int G) { return static_cast<int64_t>(max_q) * G <= b200
 template <int DQK, bool FP8, int NT>
 int launch_decode(const b200attn_paged_cache* c, PagedAttn p, int sm_count, int device, cudaStream_t st) {
   using C = b200p::DecCfg<DQK, 128, FP8, NT>;
-  p.box = gcd(p.page_size, b200p::kDecKeys);
+  p.box = gcd(p.page_size, C::KEYS);
   p.slot_rows = b200p::kDecMaxRows;
   CUtensorMap tk, tv;
   if (!page_maps(&tk, &tv, c, p.box, true)) return B200ATTN_ERR_CUDA;
@@ -380,7 +380,7 @@ int b200attn_paged_fwd(const void* q, size_t q_stride, const b200attn_paged_cach
   const int64_t keys = static_cast<int64_t>(table_width) * cache->page_size;
   if (keys >= (int64_t(1) << 31) || table_stride > 0x7fffffff ||
       static_cast<int64_t>(total) * Hq >= (int64_t(1) << 31) ||
-      static_cast<int64_t>(batch) * cache->Hkv * (keys / b200p::kDecKeys + 1) >= (int64_t(1) << 31))
+      static_cast<int64_t>(batch) * cache->Hkv * (keys / 64 /* the smallest tile */ + 1) >= (int64_t(1) << 31))
     return B200ATTN_ERR_UNSUPPORTED;
   const size_t need = b200attn_paged_fwd_workspace_bytes(total, max_seqlen_q, Hq, cache->Hkv);
   if (!workspace || workspace_bytes < need || !aligned(workspace, 16)) return B200ATTN_ERR_WORKSPACE;

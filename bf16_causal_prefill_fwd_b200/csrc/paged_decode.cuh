@@ -9,7 +9,7 @@
 // kernel is bound by HBM; what it has to do is keep loads in flight on every
 // SM, whatever the lengths.
 //
-// Split. The keys of every (request, key/value head) are cut into tiles of 64,
+// Split. The keys of every (request, key/value head) are cut into tiles (dec_keys),
 // the tiles of the whole batch form one line, and each of the resident blocks
 // takes an equal run of it: a long context is spread over many blocks and short
 // ones share a block. A unit whose tiles lie in several blocks leaves (m, l, O)
@@ -20,7 +20,7 @@
 // Block: one warp copies pages to a ring of stages in shared memory (TMA, one
 // box per page piece and 128-byte column block, 128-byte swizzle; what lies
 // behind the last page is read as zeros through an out-of-range page number);
-// four warps take 16 keys of each stage each. S^T = K Q^T (16 keys x 8 rows)
+// four warps take a quarter of each stage's keys each. S^T = K Q^T (16 keys x 8 rows)
 // puts the keys on the M side of mma.sync.m16n8k16, so that 4 to 8 rows fill the
 // N side of 8 instead of wasting half of M = 16; P^T goes from accumulator to B
 // operand with movmatrix; O^T = V^T P^T. The tensor cores' own rate is of no
@@ -36,8 +36,10 @@
 
 namespace b200p {
 
-constexpr int kDecKeys = 64;     // keys per tile (one stage of the ring)
-constexpr int kDecWarps = 4;     // consumer warps, 16 keys of a tile each
+constexpr int kDecWarps = 4;     // consumer warps
+// Keys per tile (one stage of the ring): 16 per warp, of an e4m3 cache 32, whose
+// two groups' conversions and products fill each other's gaps.
+__host__ __device__ constexpr int dec_keys(bool fp8, int d_qk) { return fp8 && d_qk == 128 ? 128 : 64; }
 constexpr int kDecThreads = 32 * (kDecWarps + 1);
 constexpr int kDecMaxBlocks = 480;  // workspace slots are sized for this many blocks
 constexpr int kDecMaxRows = 16;
@@ -47,7 +49,8 @@ struct DecCfg {
   static constexpr int ESZ = FP8 ? 1 : 2;
   static constexpr int KC = (DQK * ESZ + 127) / 128;  // 128-byte column blocks of a K row
   static constexpr int VC = (DV * ESZ + 127) / 128;
-  static constexpr int CHUNK = kDecKeys * 128;  // one column block of a tile
+  static constexpr int KEYS = dec_keys(FP8, DQK), KG = KEYS / (16 * kDecWarps);  // groups of 16 keys per warp and tile
+  static constexpr int CHUNK = KEYS * 128;  // one column block of a tile
   static constexpr int K_BYTES = KC * CHUNK, V_BYTES = VC * CHUNK;
   static constexpr int STAGE = K_BYTES + V_BYTES;
   static constexpr int MROW = DV + 4;                           // floats per row there (bank offset of 8 for two rows)
@@ -56,7 +59,7 @@ struct DecCfg {
   static constexpr int FIXED = MERGE + ML + 512 /*barriers, plan*/ + 1024 /*alignment*/;
   // Blocks per SM. Two are enough to stream bf16 pages; with e4m3 a tile is half
   // the bytes for more instructions, and a third block's warps fill the gaps.
-  static constexpr int BLOCKS = FP8 && NT == 1 ? 3 : 2;
+  static constexpr int BLOCKS = FP8 && NT == 1 && KG == 1 ? 3 : 2;
   static constexpr int BUDGET = 227 * 1024 / BLOCKS / 1024 * 1024 - (BLOCKS == 2 ? 0 : 1024);
   static constexpr int FIT = (BUDGET - FIXED) / STAGE;
   static constexpr int STAGES = FIT > 6 ? 6 : FIT;
@@ -66,8 +69,9 @@ struct DecCfg {
 
 // Tiles of one key/value head of a request: none without new tokens; a request
 // without keys still has one, which masks everything.
+template <int KEYS>
 __device__ __forceinline__ int dec_tiles(const Request& r) {
-  return r.nq == 0 ? 0 : max(1, (r.kv + kDecKeys - 1) / kDecKeys);
+  return r.nq == 0 ? 0 : max(1, (r.kv + KEYS - 1) / KEYS);
 }
 
 // A block's place in the line of tiles: request, head and tile to start at.
@@ -76,13 +80,14 @@ struct DecStart {
 };
 
 // Every thread of the block; `sm`: kDecThreads + 8 ints of shared memory.
+template <int KEYS>
 __device__ __forceinline__ DecStart dec_start(const PagedAttn& p, int* sm) {
   const int tid = threadIdx.x;
   // thread t sums requests [t * seg, (t + 1) * seg)
   const int seg = (p.B + kDecThreads - 1) / kDecThreads;
   const int b0 = min(tid * seg, p.B), b1 = min(b0 + seg, p.B);
   int sum = 0;
-  for (int b = b0; b < b1; ++b) sum += dec_tiles(paged_request(p, b, blockIdx.x == 0));
+  for (int b = b0; b < b1; ++b) sum += dec_tiles<KEYS>(paged_request(p, b, blockIdx.x == 0));
   sm[tid] = sum;
   __syncthreads();
   if (tid < 32) {
@@ -114,7 +119,7 @@ __device__ __forceinline__ DecStart dec_start(const PagedAttn& p, int* sm) {
     if (mine <= d.first && d.first < mine + sum * p.Hkv) {
       int acc = mine;
       for (int b = b0; b < b1; ++b) {
-        const int n = dec_tiles(paged_request(p, b, false));
+        const int n = dec_tiles<KEYS>(paged_request(p, b, false));
         if (d.first < acc + n * p.Hkv) {
           sm[kDecThreads + 1] = b;
           sm[kDecThreads + 2] = (d.first - acc) / n;
@@ -133,6 +138,7 @@ __device__ __forceinline__ DecStart dec_start(const PagedAttn& p, int* sm) {
 }
 
 // Walks the units of a block's run in order.
+template <int KEYS>
 struct DecWalk {
   const PagedAttn& p;
   Request r;
@@ -147,7 +153,7 @@ struct DecWalk {
     n = 0;
     if (left > 0) {
       r = paged_request(p, b, false);
-      tiles = dec_tiles(r);
+      tiles = dec_tiles<KEYS>(r);
       n = min(left, tiles - k0);
       left -= n;
     }
@@ -168,7 +174,7 @@ struct DecWalk {
           return;
         }
         r = paged_request(p, b, false);
-        tiles = dec_tiles(r);
+        tiles = dec_tiles<KEYS>(r);
       } while (tiles == 0);
     }
     n = min(left, tiles);
@@ -205,22 +211,22 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<DQK, DV, FP8, NT>::BLOCKS)
     prefetch_tmap(&tmV);
   }
   pdl_wait();
-  const DecStart d = dec_start(p, s_plan);  // its barriers order the set-up above too
+  const DecStart d = dec_start<C::KEYS>(p, s_plan);  // its barriers order the set-up above too
   __syncthreads();
   if (threadIdx.x == 0) reinterpret_cast<PartDesc*>(p.desc)[blockIdx.x].last = -1;
 
   if (warp == kDecWarps) {
     // ------------------------------------------------------------ copies
-    const int boxes = kDecKeys / p.box;  // per tile
+    const int boxes = C::KEYS / p.box;  // per tile
     const int issues = boxes * (C::KC + C::VC);
     const int ahead = 32 / boxes;        // tiles whose page numbers one load of the warp covers: a power of two
     uint32_t it = 0;
     bool ok = true;
-    for (DecWalk w(p, d); ok && w.valid(); w.next()) {
+    for (DecWalk<C::KEYS> w(p, d); ok && w.valid(); w.next()) {
       int page = 0;
       for (int k = 0; k < w.n; ++k, ++it) {
         const int kt = w.k0 + k, a = k & (ahead - 1);
-        if (a == 0) page = lane < ahead * boxes ? paged_page(p, w.b, kt * kDecKeys + lane * p.box, w.r.kv) : 0;
+        if (a == 0) page = lane < ahead * boxes ? paged_page(p, w.b, kt * C::KEYS + lane * p.box, w.r.kv) : 0;
         const uint32_t s = it % C::STAGES;
         if (it >= C::STAGES) {
           ok = paged_wait(bEmpty + 8 * s, ((it / C::STAGES) - 1) & 1, abort_flag);
@@ -234,7 +240,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<DQK, DV, FP8, NT>::BLOCKS)
         const int box = lane / (C::KC + C::VC), c = lane % (C::KC + C::VC);
         const int pg = __shfl_sync(0xffffffffu, page, a * boxes + (lane < issues ? box : 0));
         if (lane < issues) {
-          const int row = paged_row(p, kt * kDecKeys + box * p.box);
+          const int row = paged_row(p, kt * C::KEYS + box * p.box);
           const uint32_t dst = base + s * C::STAGE + c * C::CHUNK + box * p.box * 128;
           if (c < C::KC)
             tma_load_4d(dst, &tmK, bFull + 8 * s, c * (128 / C::ESZ), w.h, row, pg);
@@ -248,9 +254,9 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<DQK, DV, FP8, NT>::BLOCKS)
     // ------------------------------------------------------------ products
     uint32_t it = 0;
     bool ok = true;
-    const int key0 = 16 * warp;  // this warp's keys of a tile
+    const int key0 = 16 * C::KG * warp;  // this warp's keys of a tile
     const int mrow = (lane & 15), mhalf = lane >> 4;
-    for (DecWalk w(p, d); w.valid(); w.next()) {
+    for (DecWalk<C::KEYS> w(p, d); w.valid(); w.next()) {
       const int nrows = w.r.nq * p.G;
       // Q^T as B operand: row n = lane / 4 of each group of eight
       constexpr int KS = DQK / 16;
@@ -327,24 +333,26 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<DQK, DV, FP8, NT>::BLOCKS)
         if (ok) ok = paged_wait(bFull + 8 * s, (it / C::STAGES) & 1, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         const uint32_t sk = base + s * C::STAGE, sv = sk + C::K_BYTES;
-        const int kv0 = (w.k0 + k) * kDecKeys + key0;  // first key of this warp
-        if (kv0 + 16 > w.r.kv) {
+        const int kv0 = (w.k0 + k) * C::KEYS + key0;  // first key of this warp
+        if (kv0 + 16 * C::KG > w.r.kv) {
           // Rows behind the last key may hold anything; a probability of zero
           // does not silence a NaN, so their values are cleared.
           const int from = max(0, w.r.kv - kv0);
-          for (int i = lane; i < (16 - from) * C::VC * 8; i += 32) {
+          for (int i = lane; i < (16 * C::KG - from) * C::VC * 8; i += 32) {
             const int row = key0 + from + i / (C::VC * 8), c = (i / 8) % C::VC;
             st_shared_v4(sv + c * C::CHUNK + row * 128 + 16 * (i & 7), 0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
           __syncwarp();
         }
-        // S^T = K Q^T
-        float sc[NT][4], sd[NT][4];
+        // S^T = K Q^T; the products of even and odd steps in accumulators of their own
+        float sc[C::KG][NT][4], sd[C::KG][NT][4];
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int gi = 0; gi < C::KG; ++gi)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sc[j][i] = sd[j][i] = 0.0f;
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sc[gi][j][i] = sd[gi][j][i] = 0.0f;
         if constexpr (!FP8) {
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) {
@@ -352,40 +360,48 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<DQK, DV, FP8, NT>::BLOCKS)
             uint32_t a[4];
             ldsm_x4(sk + (u >> 3) * C::CHUNK + row * 128 + (((u & 7) ^ (row & 7)) << 4), a);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) mma16816<false>((ks & 1) ? sd[j] : sc[j], a, qf[j][ks][0], qf[j][ks][1]);
+            for (int j = 0; j < NT; ++j)
+              mma16816<false>((ks & 1) ? sd[0][j] : sc[0][j], a, qf[j][ks][0], qf[j][ks][1]);
           }
         } else {
 #pragma unroll
           for (int ks = 0; ks < KS; ks += 2) {
-            const int u = ks + mhalf, row = key0 + mrow;
-            uint32_t c[4];  // (keys 0-7, 8-15) of unit ks, then of unit ks + 1
-            ldsm_x4(sk + (u >> 3) * C::CHUNK + row * 128 + (((u & 7) ^ (row & 7)) << 4), c);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t a[4] = {e4m3x2_f16x2(c[2 * i]), e4m3x2_f16x2(c[2 * i + 1]), e4m3x2_f16x2(c[2 * i] >> 16),
-                                     e4m3x2_f16x2(c[2 * i + 1] >> 16)};
+            for (int gi = 0; gi < C::KG; ++gi) {
+              const int u = ks + mhalf, row = key0 + 16 * gi + mrow;
+              uint32_t c[4];  // (keys 0-7, 8-15) of unit ks, then of unit ks + 1
+              ldsm_x4(sk + (u >> 3) * C::CHUNK + row * 128 + (((u & 7) ^ (row & 7)) << 4), c);
 #pragma unroll
-              for (int j = 0; j < NT; ++j)
-                mma16816<true>(i ? sd[j] : sc[j], a, qf[j][ks + i][0], qf[j][ks + i][1]);
+              for (int i = 0; i < 2; ++i) {
+                const uint32_t a[4] = {e4m3x2_f16x2(c[2 * i]), e4m3x2_f16x2(c[2 * i + 1]),
+                                       e4m3x2_f16x2(c[2 * i] >> 16), e4m3x2_f16x2(c[2 * i + 1] >> 16)};
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                  mma16816<true>(i ? sd[gi][j] : sc[gi][j], a, qf[j][ks + i][0], qf[j][ks + i][1]);
+              }
             }
           }
         }
-        uint32_t pb[NT][2];
+        uint32_t pb[C::KG][NT][2];
         float alpha[NT][2];
         bool moved = false;
-        const bool edge = kv0 + 15 > all_see;
+        const bool edge = kv0 + 16 * C::KG - 1 > all_see;
         const int kl = kv0 + (lane >> 2);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          float x[4];
+          float x[C::KG][4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[i] = (sc[j][i] + sd[j][i]) * cs[j][i & 1];
-            if (edge && kl + 8 * (i >> 1) > see[j][i & 1]) x[i] = -INFINITY;
-          }
+          for (int gi = 0; gi < C::KG; ++gi)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x[gi][i] = (sc[gi][j][i] + sd[gi][j][i]) * cs[j][i & 1];
+              if (edge && kl + 16 * gi + 8 * (i >> 1) > see[j][i & 1]) x[gi][i] = -INFINITY;
+            }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float mx = fmaxf(x[i], x[i + 2]);
+            float mx = fmaxf(x[0][i], x[0][i + 2]);
+#pragma unroll
+            for (int gi = 1; gi < C::KG; ++gi) mx = fmaxf(mx, fmaxf(x[gi][i], x[gi][i + 2]));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -394,16 +410,19 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<DQK, DV, FP8, NT>::BLOCKS)
             moved |= mn > m[j][i];
             m[j][i] = mn;
             const float ref = mn == -INFINITY ? 0.0f : mn;  // nothing seen yet: every probability is 0
-            x[i] = ex2_approx(x[i] - ref);
-            x[i + 2] = ex2_approx(x[i + 2] - ref);
-            l[j][i] = fmaf(l[j][i], alpha[j][i], x[i] + x[i + 2]);
+            float sum = 0.0f;
+#pragma unroll
+            for (int gi = 0; gi < C::KG; ++gi) {
+              x[gi][i] = ex2_approx(x[gi][i] - ref);
+              x[gi][i + 2] = ex2_approx(x[gi][i + 2] - ref);
+              sum += x[gi][i] + x[gi][i + 2];
+            }
+            l[j][i] = fmaf(l[j][i], alpha[j][i], sum);
           }
-          if constexpr (FP8) {
-            pb[j][0] = movm_t(pack_f16x2(x[0], x[1]));
-            pb[j][1] = movm_t(pack_f16x2(x[2], x[3]));
-          } else {
-            pb[j][0] = movm_t(pack_bf16x2(x[0], x[1]));
-            pb[j][1] = movm_t(pack_bf16x2(x[2], x[3]));
+#pragma unroll
+          for (int gi = 0; gi < C::KG; ++gi) {
+            pb[gi][j][0] = movm_t(FP8 ? pack_f16x2(x[gi][0], x[gi][1]) : pack_bf16x2(x[gi][0], x[gi][1]));
+            pb[gi][j][1] = movm_t(FP8 ? pack_f16x2(x[gi][2], x[gi][3]) : pack_bf16x2(x[gi][2], x[gi][3]));
           }
         }
         if (__any_sync(0xffffffffu, moved)) {
@@ -423,23 +442,26 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<DQK, DV, FP8, NT>::BLOCKS)
             uint32_t a[4];
             ldsm_x4_t(sv + (u >> 3) * C::CHUNK + row * 128 + (((u & 7) ^ (row & 7)) << 4), a);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) mma16816<false>(o[t][j], a, pb[j][0], pb[j][1]);
+            for (int j = 0; j < NT; ++j) mma16816<false>(o[t][j], a, pb[0][j][0], pb[0][j][1]);
           }
         } else {
 #pragma unroll
           for (int t = 0; t < DV / 16; t += 2) {
-            // (keys 0-7, 8-15) of unit t, then of unit t + 1; a transposed pair of
-            // codes is (d = 2g, 2g + 1): even d on rows 0-7 of M, odd on 8-15
-            const int row = key0 + (lane & 15), u = t + mhalf;
-            uint32_t c[4];
-            ldsm_x4_t(sv + row * 128 + ((u ^ (row & 7)) << 4), c);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t lo = c[2 * i], hi = c[2 * i + 1];
-              const uint32_t a[4] = {e4m3x2_f16x2(prmt(lo, 0u, 0x4420u)), e4m3x2_f16x2(prmt(lo, 0u, 0x4431u)),
-                                     e4m3x2_f16x2(prmt(hi, 0u, 0x4420u)), e4m3x2_f16x2(prmt(hi, 0u, 0x4431u))};
+            for (int gi = 0; gi < C::KG; ++gi) {
+              // (keys 0-7, 8-15) of unit t, then of unit t + 1; a transposed pair of
+              // codes is (d = 2g, 2g + 1): even d on rows 0-7 of M, odd on 8-15
+              const int row = key0 + 16 * gi + (lane & 15), u = t + mhalf;
+              uint32_t c[4];
+              ldsm_x4_t(sv + row * 128 + ((u ^ (row & 7)) << 4), c);
 #pragma unroll
-              for (int j = 0; j < NT; ++j) mma16816<true>(o[t + i][j], a, pb[j][0], pb[j][1]);
+              for (int i = 0; i < 2; ++i) {
+                const uint32_t lo = c[2 * i], hi = c[2 * i + 1];
+                const uint32_t a[4] = {e4m3x2_f16x2(prmt(lo, 0u, 0x4420u)), e4m3x2_f16x2(prmt(lo, 0u, 0x4431u)),
+                                       e4m3x2_f16x2(prmt(hi, 0u, 0x4420u)), e4m3x2_f16x2(prmt(hi, 0u, 0x4431u))};
+#pragma unroll
+                for (int j = 0; j < NT; ++j) mma16816<true>(o[t + i][j], a, pb[gi][j][0], pb[gi][j][1]);
+              }
             }
           }
         }
