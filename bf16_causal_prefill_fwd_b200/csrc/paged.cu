@@ -346,7 +346,9 @@ int b200attn_paged_append(const void* k, const void* v, size_t k_stride, size_t 
   p.page_size = b200p::fast_div(cache->page_size);
   p.per_token = b200p::fast_div(cache->Hkv * ((cache->d_qk + cache->d_v) / b200p::kAppendUnit));
   const int64_t want = (units + b200p::kAppendThreads - 1) / b200p::kAppendThreads;
-  const int blocks = static_cast<int>(want < 8 * sm_count ? want : 8 * sm_count);
+  // One unit per thread while the grid is below 64 blocks per SM: measured on 16k tokens, 8 blocks per SM looping
+  // take 23.6 us (bf16) and 20.7 us (e4m3), 64 take 20.7 and 19.4; two or four units in flight per thread were slower.
+  const int blocks = static_cast<int>(want < 64 * sm_count ? want : 64 * sm_count);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   auto kern = cache->dtype == B200ATTN_BF16
                   ? (cache->d_qk == 128 ? b200p::paged_append_kernel<128, 128, false> : b200p::paged_append_kernel<192, 128, false>)
