@@ -92,6 +92,11 @@ int prepare_kernel(const void* kern, int bytes, int regs, int device, std::atomi
 // A stride the kernels may use: a multiple of 16 bytes, not negative.
 bool stride_ok(int64_t elems, int esz) { return elems >= 0 && elems < (int64_t(1) << 38) && elems * esz % 16 == 0; }
 
+// The distance of tokens of `heads` contiguous heads: they do not overlap.
+bool rows_ok(size_t stride, int tokens, int heads, int d) {
+  return tokens == 1 || (stride_ok(static_cast<int64_t>(stride), 2) && static_cast<int64_t>(stride) >= int64_t(heads) * d);
+}
+
 // Argument checks that every entry point taking a cache shares.
 int check_cache(const b200attn_paged_cache* c) {
   if (!c || !c->k || !c->v) return B200ATTN_ERR_INVALID;
@@ -104,8 +109,9 @@ int check_cache(const b200attn_paged_cache* c) {
   const int esz = c->dtype == B200ATTN_BF16 ? 2 : 1;
   const int64_t s[6] = {c->k_page_stride, c->k_token_stride, c->k_head_stride,
                         c->v_page_stride, c->v_token_stride, c->v_head_stride};
-  for (int64_t x : s)
-    if (!stride_ok(x, esz)) return B200ATTN_ERR_INVALID;
+  const int size[3] = {c->num_pages, c->page_size, c->Hkv};
+  for (int i = 0; i < 6; ++i)  // the stride of a dimension of one is not used
+    if (size[i % 3] > 1 && (s[i] == 0 || !stride_ok(s[i], esz))) return B200ATTN_ERR_INVALID;
   if (c->dtype == B200ATTN_FP8_E4M3 &&
       (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)))
     return B200ATTN_ERR_INVALID;
@@ -316,7 +322,8 @@ int b200attn_paged_append(const void* k, const void* v, size_t k_stride, size_t 
   if (total < 0) return B200ATTN_ERR_INVALID;
   if (total == 0) return B200ATTN_OK;
   if (!k || !v || !slots || !aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4)) return B200ATTN_ERR_INVALID;
-  if (!stride_ok(static_cast<int64_t>(k_stride), 2) || !stride_ok(static_cast<int64_t>(v_stride), 2)) return B200ATTN_ERR_INVALID;
+  if (!rows_ok(k_stride, total, cache->Hkv, cache->d_qk) || !rows_ok(v_stride, total, cache->Hkv, cache->d_v))
+    return B200ATTN_ERR_INVALID;
   const int64_t units =
       static_cast<int64_t>(total) * cache->Hkv * ((cache->d_qk + cache->d_v) / b200p::kAppendUnit);
   if (units >= (int64_t(1) << 31)) return B200ATTN_ERR_UNSUPPORTED;
@@ -374,13 +381,13 @@ int b200attn_paged_fwd(const void* q, size_t q_stride, const b200attn_paged_cach
   if (total == 0) return B200ATTN_OK;  // no new tokens
   if (!q || !o || !block_table || !cu_seqlens || !kv_lens) return B200ATTN_ERR_INVALID;
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(block_table, 4) || !aligned(cu_seqlens, 4) ||
-      !aligned(kv_lens, 4) || !aligned(lse, 4) || !stride_ok(static_cast<int64_t>(q_stride), 2))
+      !aligned(kv_lens, 4) || !aligned(lse, 4) || !rows_ok(q_stride, total, Hq, cache->d_qk))
     return B200ATTN_ERR_INVALID;
   const int G = Hq / cache->Hkv;
   if (G > 128) return B200ATTN_ERR_UNSUPPORTED;
   // the kernels count query rows and key tiles in 32 bits
   const int64_t keys = static_cast<int64_t>(table_width) * cache->page_size;
-  if (keys >= (int64_t(1) << 31) || table_stride > 0x7fffffff ||
+  if (keys >= (int64_t(1) << 30) || table_stride > 0x7fffffff ||
       static_cast<int64_t>(total) * Hq >= (int64_t(1) << 31) ||
       static_cast<int64_t>(batch) * cache->Hkv * (keys / 64 /* the smallest tile */ + 1) >= (int64_t(1) << 31))
     return B200ATTN_ERR_UNSUPPORTED;

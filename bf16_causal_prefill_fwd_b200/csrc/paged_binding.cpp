@@ -106,12 +106,13 @@ struct Rows {
 Rows rows_of(PyObject* o, const char* name, int64_t d, const c10::Device& dev) {
   const at::Tensor* t = tensor(o);
   if (t && t->scalar_type() == at::kBFloat16 && t->dim() == 3 && t->device() == dev) {
-    const int64_t n = t->size(0), h = t->size(1), stride = t->stride(0);
-    if (t->size(2) == d && h > 0 && t->stride(2) == 1 && (h == 1 || t->stride(1) == d) && stride >= 0 && stride % 8 == 0)
+    const int64_t n = t->size(0), h = t->size(1), stride = n > 1 ? t->stride(0) : h * d;
+    if (t->size(2) == d && h > 0 && t->stride(2) == 1 && (h == 1 || t->stride(1) == d) && stride >= h * d &&
+        stride % 8 == 0)
       return {t, n, h, stride};
   }
   refuse(name, "bf16 [tokens, heads, " + std::to_string(d) + "] on " + dev.str() +
-                   " with contiguous heads and a token stride that is a multiple of 8 elements", o);
+                   " with contiguous heads, tokens that do not overlap and are a multiple of 8 elements apart", o);
 }
 
 // The cache tensors as the library takes them.

@@ -127,15 +127,36 @@ struct ChStart {
   int b, h, pair, skip, count, first, per;
 };
 
-// A block's run of the line. Every thread of the block; `sm`: THREADS + 8 ints.
+// Whether the sum of `mine` over the block stays below 2^31 (the slow answer, for
+// when no part of it alone says so).
+template <int THREADS>
+__device__ __noinline__ bool ch_line_fits(int64_t mine, long long* sm) {
+  sm[threadIdx.x] = mine;
+  __syncthreads();
+  long long all = 0;
+  for (int i = 0; i < THREADS; ++i) all += sm[i];
+  __syncthreads();
+  return all < (1ll << 31);
+}
+
+// A block's run of the line. Every thread of the block; `sm`: 2 THREADS ints.
 template <int THREADS>
 __device__ __forceinline__ ChStart ch_start(const PagedAttn& p, int tpt, int* sm) {
   const int tid = threadIdx.x;
   const int seg = (p.B + THREADS - 1) / THREADS;
   const int b0 = min(tid * seg, p.B), b1 = min(b0 + seg, p.B);
-  int sum = 0;
+  // Requests whose rows overlap (a cu_seqlens that goes back) can make the line
+  // longer than the host's check allows for: counted in 64 bits, and then refused.
+  int64_t sum = 0;
   for (int b = b0; b < b1; ++b) sum += ch_head_cost(paged_request(p, b, blockIdx.x == 0), tpt, p.causal);
-  sm[tid] = sum;
+  const bool fits = __syncthreads_and(sum * p.Hkv < (int64_t(1) << 31) / THREADS) ||
+                    ch_line_fits<THREADS>(sum * p.Hkv, reinterpret_cast<long long*>(sm));
+  if (!fits) {
+    if (blockIdx.x == 0 && tid == 0) paged_report(kPagedInvalid);
+    sum = 0;
+  }
+  sm[tid] = static_cast<int>(sum);
+  if (tid < 4) sm[THREADS + 1 + tid] = 0;
   __syncthreads();
   if (tid < 32) {
     constexpr int per_lane = THREADS / 32;
@@ -163,7 +184,7 @@ __device__ __forceinline__ ChStart ch_start(const PagedAttn& p, int tpt, int* sm
   d.count = max(0, min(d.per, total - d.first));
   if (d.count > 0) {
     int acc = sm[tid] * p.Hkv;
-    if (acc <= d.first && d.first < acc + sum * p.Hkv) {
+    if (acc <= d.first && d.first < acc + static_cast<int>(sum) * p.Hkv) {
       for (int b = b0; b < b1; ++b) {
         const Request r = paged_request(p, b, false);
         const int n = ch_head_cost(r, tpt, p.causal);

@@ -89,6 +89,7 @@ __device__ __forceinline__ DecStart dec_start(const PagedAttn& p, int* sm) {
   int sum = 0;
   for (int b = b0; b < b1; ++b) sum += dec_tiles<KEYS>(paged_request(p, b, blockIdx.x == 0));
   sm[tid] = sum;
+  if (tid < 3) sm[kDecThreads + 1 + tid] = 0;
   __syncthreads();
   if (tid < 32) {
     constexpr int per_lane = kDecThreads / 32;

@@ -342,6 +342,30 @@ def test_contents_that_do_not_fit_are_skipped_and_reported(max_q):
     assert torch.equal(b2.attn_paged_fwd(*good.args(), max_seqlen_q=max_q), want) and b2.check() == 0
 
 
+def test_requests_that_share_rows_stay_in_bounds():
+    """A cu_seqlens that goes back and forth gives every second request all rows: each is computed, rows keep one of
+    the results, and a line of work past 32-bit counts is refused."""
+    n, B = 64, 8
+    p = make([n] * B, [100] * B, 8, 2, 128, 16, seed=33)
+    d = p.cuda()
+    d.cu.copy_(torch.tensor([0, n] * (B // 2) + [0], dtype=torch.int32))
+    out = torch.full((n * B, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    b2.attn_paged_fwd(*d.args(), out=out)
+    assert b2.check() == -1
+    assert not bool(out.isnan().any()) and bool((out[n:] == 7.0).all())
+    # 2000 requests that all have the same 65536 rows, over 1050 key blocks: 2000 * 1024 pairs of row tiles * 1050
+    B, T, pages = 4000, 65536, 2100
+    kc = torch.zeros(1, 64, 1, 128, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(T, 4, 128, dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros(B, pages, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, T] * (B // 2) + [0], dtype=torch.int32, device="cuda")
+    kv = torch.full((B,), 64 * pages, dtype=torch.int32, device="cuda")
+    assert (B // 2) * (T // 64) * (64 * pages // 128) >= 2 ** 31
+    out = torch.full((T, 4, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    b2.attn_paged_fwd(q, kc, kc, table, cu, kv, causal=False, out=out)
+    assert b2.check() == -1 and bool((out == 7.0).all())
+
+
 @pytest.mark.parametrize("n,max_q", [(1, 1), (20, 20)])
 def test_table_entries_that_are_no_page_read_as_zeros(n, max_q):
     p = make([n, n], [60, 90], 8, 2, 128, 16, seed=22)

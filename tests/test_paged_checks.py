@@ -124,6 +124,7 @@ def test_no_new_tokens_is_no_work(lib):
 @pytest.mark.parametrize("bad", [
     dict(q=torch.zeros(T, HQ, D)), dict(q=bf16(T, HQ, 64)), dict(q=bf16(T, 7, D)), dict(q=bf16(T, HQ * D)),
     dict(q=bf16(T, D, HQ).transpose(1, 2)), dict(q=bf16(T, HQ * D + 4)[:, : HQ * D].unflatten(1, (HQ, D))),
+    dict(q=bf16(1, HQ, D).expand(T, HQ, D)), dict(q=bf16(T, HQ, D).as_strided((T, HQ, D), (D, D, 1))),
     dict(kc=bf16(P, PS, HKV, D).float()), dict(kc=bf16(P, PS, 3, D)), dict(vc=bf16(P + 1, PS, HKV, D)),
     dict(kc=bf16(PS, HKV, D)), dict(kc=bf16(P, PS, D, HKV).transpose(2, 3)),
     dict(kc=bf16(P, PS, HKV, D + 4)[..., :D]), dict(kc=bf16(1, PS, HKV, D).expand(P, PS, HKV, D)),
@@ -196,15 +197,15 @@ def c_attn(lib, c, q=FAKE, stride=HQ * D, table=FAKE, row=W, width=W, cu=FAKE, k
 
 def test_attn_entry_point_refuses(real):
     assert c_attn(real, None) == -1
-    for bad in (dict(k=0), dict(v=FAKE + 8), dict(pages=0), dict(ps=0), dict(page=12), dict(token=-8), dict(dtype=1)):
+    for bad in (dict(k=0), dict(v=FAKE + 8), dict(pages=0), dict(ps=0), dict(page=12), dict(token=-8), dict(head=0), dict(dtype=1)):
         assert c_attn(real, cache(**bad)) == -1, bad
     for bad in (dict(ps=24), dict(dqk=64), dict(dv=64), dict(dtype=7), dict(pages=1 << 28)):
         assert c_attn(real, cache(**bad)) == -2, bad
-    for bad in (dict(q=None), dict(q=FAKE + 2), dict(stride=4), dict(table=None), dict(width=0), dict(cu=None), dict(kv=None),
+    for bad in (dict(q=None), dict(q=FAKE + 2), dict(stride=4), dict(stride=0), dict(stride=8), dict(table=None), dict(width=0), dict(cu=None), dict(kv=None),
                 dict(batch=0), dict(total=-1), dict(maxq=0), dict(hq=3), dict(causal=2), dict(scale=float("nan")), dict(o=None),
                 dict(lse=FAKE + 2), dict(cu=FAKE + 1)):
         assert c_attn(real, cache(), **bad) == -1, bad
-    assert c_attn(real, cache(h=1), hq=129) == -2                     # a group of more than 128 heads
+    assert c_attn(real, cache(h=1), hq=129, stride=129 * D) == -2                     # a group of more than 128 heads
     assert c_attn(real, cache(), width=(1 << 27) + 1) == -2           # keys past 32-bit counts
     assert c_attn(real, cache(), total=1 << 28, hq=HQ) == -2          # rows past 32-bit counts
     assert c_attn(real, cache(), ws=None) == -5
@@ -221,7 +222,7 @@ def test_append_entry_point_refuses(real):
     assert call(cache(ps=8)) == -2
     for bad in (dict(k=None), dict(v=FAKE + 8), dict(ks=4), dict(total=-1), dict(s=None), dict(s=FAKE + 2)):
         assert call(cache(), **bad) == -1, bad
-    assert call(cache(h=1 << 16), total=1 << 20) == -2                # units past 32 bits
+    assert call(cache(h=1 << 16), ks=D << 16, vs=D << 16, total=1 << 20) == -2                # units past 32 bits
     assert call(cache(), total=0, k=None) == 0
 
 
