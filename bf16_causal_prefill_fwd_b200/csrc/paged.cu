@@ -14,6 +14,7 @@
 #include "paged_chunk.cuh"
 #include "paged_common.cuh"
 #include "paged_decode.cuh"
+#include "paged_join.cuh"
 #include "paged_slots.cuh"
 #include "paged_status.h"
 
@@ -208,7 +209,7 @@ int launch_decode(const b200attn_paged_cache* c, PagedAttn p, int sm_count, int 
   const int lrc = launch(kern, dim3(blocks, 1, 1), b200p::kDecThreads, C::SMEM, 1, st, static_cast<const CUtensorMap>(tk),
                          static_cast<const CUtensorMap>(tv), static_cast<const PagedAttn>(p));
   if (lrc != B200ATTN_OK) return lrc;
-  return launch(b200p::paged_join_kernel<128>, dim3(blocks, 4, 1), 128, 0, 1, st, static_cast<const PagedAttn>(p));
+  return launch(b200p::paged_join_few_kernel<128>, dim3(blocks, 4, 1), 128, 0, 1, st, static_cast<const PagedAttn>(p));
 }
 
 template <int DQK, bool FP8>
@@ -228,6 +229,7 @@ int launch_chunk(const b200attn_paged_cache* c, PagedAttn p, int sm_count, int d
   using C = b200p::ChCfg<DQK, 128, FP8>;
   p.box = gcd(p.page_size, b200p::kChN);
   p.slot_rows = chunk_rows(p.T, p.G);
+  p.pair = b200p::fast_div(2 * (b200p::kChM / p.G));
   CUtensorMap tq = {}, tk = {}, tv = {};
   if (!FP8) {
     // {d, head, token} with a box of 64 columns, the G heads of a group and a tile's tokens
@@ -251,7 +253,7 @@ int launch_chunk(const b200attn_paged_cache* c, PagedAttn p, int sm_count, int d
                          static_cast<const CUtensorMap>(tk), static_cast<const CUtensorMap>(tv),
                          static_cast<const PagedAttn>(p));
   if (lrc != B200ATTN_OK) return lrc;
-  return launch(b200p::paged_join_kernel<128>, dim3(blocks, p.slot_rows < 16 ? 4 : 16, 1), 128, 0, 1, st,
+  return launch(b200p::paged_join_rows_kernel<128>, dim3(blocks, (p.slot_rows + 15) / 16, 1), 128, 0, 1, st,
                 static_cast<const PagedAttn>(p));
 }
 

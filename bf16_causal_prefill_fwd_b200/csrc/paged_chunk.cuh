@@ -17,8 +17,8 @@
 // its key blocks of 128. The blocks of all units (and a fixed cost per unit) form
 // one line that is cut into equal runs, one per SM: a step of few units still uses every SM, and no SM
 // waits for a longer unit. A unit cut by a run's end leaves (m, l, O) per part,
-// joined in block order by paged_join_kernel. Every block finds its run from
-// the lengths in device memory.
+// joined in block order (paged_join.cuh). Every block finds its run from the
+// lengths in device memory.
 //
 // Keys and values. One warp copies K, one V, page piece by page piece (TMA,
 // 128-byte swizzle; pages behind the last are read as zeros through an
@@ -63,7 +63,7 @@ struct ChCfg {
   static constexpr int THREADS = 384, REGS_LAUNCH = 168;
   // Register split by warpgroup: copies and issue, softmax; the sum stays within
   // what the block was launched with.
-  static constexpr int REGS_CTRL = FP8 ? (DQK == 128 ? 80 : 104) : 72, REGS_SOFT = FP8 ? 200 : 208;
+  static constexpr int REGS_CTRL = FP8 ? 104 : 72, REGS_SOFT = FP8 ? 200 : 208;
   static_assert(128 * REGS_CTRL + 256 * REGS_SOFT <= THREADS * REGS_LAUNCH, "registers");
   static constexpr int CHUNK = kChM * 128;  // 128 rows x 128 bytes, swizzled
   static constexpr int KSZ = FP8 ? 1 : 2;
@@ -77,7 +77,7 @@ struct ChCfg {
   static constexpr int SK_FIT = (AVAIL - SV * V_BYTES) / K_BYTES, SK = SK_FIT > 4 ? 4 : SK_FIT;
   static constexpr int BARS = 2 + 2 + 2 * SK + 2 * SV + 1 + 6 + 2 + 1 + 2 + 2 + 2 + 2 + 2 + 2 * kChUnits;
   static constexpr int SMEM = 2 * Q_BYTES + SK * K_BYTES + SV * V_BYTES + STAGES * VC_BYTES + 1024 + 1024;
-  static_assert(8 * BARS + 8 + 32 <= 512 && 512 + kChUnits * 64 <= 1024 && SMEM <= 227 * 1024 && SK >= 2, "shared memory");
+  static_assert(8 * BARS + 8 <= 512 && 512 + kChUnits * 64 <= 1024 && SMEM <= 227 * 1024 && SK >= 2, "shared memory");
   // Tensor memory: S [0, 128) for both tiles in turn, O_t at 128 + 128 t, P_t
   // (16-bit, 64 columns) at 384 + 64 t.
   static constexpr int TM_O = 128, TM_P = 384;
@@ -105,15 +105,47 @@ __device__ __forceinline__ int ch_pair_blocks(const Request& r, int p, int tpt, 
   return max(ch_blocks(r, 2 * p, tpt, causal), ch_blocks(r, 2 * p + 1, tpt, causal));
 }
 
-__device__ __forceinline__ int ch_pairs(const Request& r, int tpt) { return (r.nq + 2 * tpt - 1) / (2 * tpt); }
+// sum of floor((a i + b) / m) over i = 0 .. n - 1 (a, b >= 0), by exchanging the
+// roles of a and m as in Euclid's algorithm: a few steps, whatever n.
+__device__ __forceinline__ int floor_sum(int n, int m, int a, int b) {
+  int s = 0;
+  while (true) {
+    if (a >= m) {
+      const int q = a / m;
+      s += static_cast<int>(static_cast<int64_t>(n) * (n - 1) / 2) * q;
+      a -= q * m;
+    }
+    if (b >= m) {
+      const int q = b / m;
+      s += n * q;
+      b -= q * m;
+    }
+    const int64_t y = static_cast<int64_t>(a) * n + b;  // < 2^31 where it goes on: it counts keys
+    if (y < m) return s;
+    n = static_cast<uint32_t>(y) / static_cast<uint32_t>(m);
+    b = static_cast<int>(y) - n * m;
+    const int t = m;
+    m = a;
+    a = t;
+  }
+}
+
+__device__ __forceinline__ int ch_pairs(const PagedAttn& p, const Request& r, int tpt) {
+  return static_cast<uint32_t>(r.nq + 2 * tpt - 1) / p.pair;
+}
 
 // Length in the line of the units of one key/value head of a request.
-__device__ __forceinline__ int ch_head_cost(const Request& r, int tpt, int causal) {
-  const int n = ch_pairs(r, tpt);
+__device__ __forceinline__ int ch_head_cost(const PagedAttn& p, const Request& r, int tpt) {
+  const int n = ch_pairs(p, r, tpt);
   if (n == 0) return 0;
-  if (!causal) return n * (ch_pair_blocks(r, 0, tpt, causal) + kChUnitCost);
+  if (!p.causal) return n * (ch_pair_blocks(r, 0, tpt, 0) + kChUnitCost);
   int s = n * kChUnitCost;
-  for (int p = 0; p < n; ++p) s += ch_pair_blocks(r, p, tpt, causal);
+  if (n > 4 && r.kv >= r.nq) {
+    // every pair but the last sees kv - nq + 2 tpt (i + 1) keys, the last one all
+    s += floor_sum(n - 1, kChN, 2 * tpt, r.kv - r.nq + 2 * tpt + kChN - 1) + (r.kv + kChN - 1) / kChN;
+  } else {
+    for (int i = 0; i < n; ++i) s += ch_pair_blocks(r, i, tpt, 1);
+  }
   return s;
 }
 
@@ -127,85 +159,34 @@ struct ChStart {
   int b, h, pair, skip, count, first, per;
 };
 
-// Whether the sum of `mine` over the block stays below 2^31 (the slow answer, for
-// when no part of it alone says so).
-template <int THREADS>
-__device__ __noinline__ bool ch_line_fits(int64_t mine, long long* sm) {
-  sm[threadIdx.x] = mine;
-  __syncthreads();
-  long long all = 0;
-  for (int i = 0; i < THREADS; ++i) all += sm[i];
-  __syncthreads();
-  return all < (1ll << 31);
-}
-
-// A block's run of the line. Every thread of the block; `sm`: 2 THREADS ints.
-template <int THREADS>
-__device__ __forceinline__ ChStart ch_start(const PagedAttn& p, int tpt, int* sm) {
-  const int tid = threadIdx.x;
-  const int seg = (p.B + THREADS - 1) / THREADS;
-  const int b0 = min(tid * seg, p.B), b1 = min(b0 + seg, p.B);
-  // Requests whose rows overlap (a cu_seqlens that goes back) can make the line
-  // longer than the host's check allows for: counted in 64 bits, and then refused.
-  int64_t sum = 0;
-  for (int b = b0; b < b1; ++b) sum += ch_head_cost(paged_request(p, b, blockIdx.x == 0), tpt, p.causal);
-  const bool fits = __syncthreads_and(sum * p.Hkv < (int64_t(1) << 31) / THREADS) ||
-                    ch_line_fits<THREADS>(sum * p.Hkv, reinterpret_cast<long long*>(sm));
-  if (!fits) {
-    if (blockIdx.x == 0 && tid == 0) paged_report(kPagedInvalid);
-    sum = 0;
-  }
-  sm[tid] = static_cast<int>(sum);
-  if (tid < 4) sm[THREADS + 1 + tid] = 0;
-  __syncthreads();
-  if (tid < 32) {
-    constexpr int per_lane = THREADS / 32;
-    int s = 0;
-    for (int i = 0; i < per_lane; ++i) s += sm[tid * per_lane + i];
-    int inc = s;
+// By one warp of the block.
+__device__ __forceinline__ ChStart ch_start(const PagedAttn& p, int tpt) {
+  const int lane = threadIdx.x & 31;
+  const Run run = plan_run(p, [&](const Request& x) { return ch_head_cost(p, x, tpt); });
+  ChStart d = {run.b, 0, 0, 0, run.count, run.first, run.per};
+  if (run.count == 0) return d;
+  const Request r = paged_request(p, run.b, false);
+  const int n = max(1, ch_head_cost(p, r, tpt)), pairs = ch_pairs(p, r, tpt);
+  d.h = run.off / n;
+  int off = run.off - d.h * n;
+  for (int i0 = 0; i0 < pairs; i0 += 32) {  // the pair that `off` lies in, 32 at a time
+    const int x = i0 + lane < pairs ? ch_pair_blocks(r, i0 + lane, tpt, p.causal) + kChUnitCost : 0;
+    int inc = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, inc, o);
-      if (tid >= o) inc += u;
+      if (lane >= o) inc += u;
     }
-    int run = inc - s;
-    for (int i = 0; i < per_lane; ++i) {
-      const int v = sm[tid * per_lane + i];
-      sm[tid * per_lane + i] = run;
-      run += v;
+    const uint32_t past = __ballot_sync(0xffffffffu, off < inc);
+    if (past != 0) {
+      const int at = __ffs(past) - 1;
+      d.pair = i0 + at;
+      d.skip = __shfl_sync(0xffffffffu, off - (inc - x), at);
+      return d;
     }
-    if (tid == 31) sm[THREADS] = inc;
+    off -= __shfl_sync(0xffffffffu, inc, 31);
   }
-  __syncthreads();
-  ChStart d;
-  const int total = sm[THREADS] * p.Hkv;
-  d.per = (total + gridDim.x - 1) / static_cast<int>(gridDim.x);
-  d.first = blockIdx.x * d.per;
-  d.count = max(0, min(d.per, total - d.first));
-  if (d.count > 0) {
-    int acc = sm[tid] * p.Hkv;
-    if (acc <= d.first && d.first < acc + static_cast<int>(sum) * p.Hkv) {
-      for (int b = b0; b < b1; ++b) {
-        const Request r = paged_request(p, b, false);
-        const int n = ch_head_cost(r, tpt, p.causal);
-        if (d.first < acc + n * p.Hkv) {
-          int at = (d.first - acc) % n, pair = 0;
-          for (int m; at >= (m = ch_pair_blocks(r, pair, tpt, p.causal) + kChUnitCost); ++pair) at -= m;
-          sm[THREADS + 1] = b;
-          sm[THREADS + 2] = (d.first - acc) / n;
-          sm[THREADS + 3] = pair;
-          sm[THREADS + 4] = at;
-          break;
-        }
-        acc += n * p.Hkv;
-      }
-    }
-  }
-  __syncthreads();
-  d.b = sm[THREADS + 1];
-  d.h = sm[THREADS + 2];
-  d.pair = sm[THREADS + 3];
-  d.skip = sm[THREADS + 4];
+  d.count = 0;  // lengths that changed while being read
   return d;
 }
 
@@ -218,29 +199,29 @@ __device__ __forceinline__ ChStart ch_start(const PagedAttn& p, int tpt, int* sm
 // Only the K warp walks; the other roles read what it finds (ChUnit).
 struct ChWalk {
   const PagedAttn& p;
-  const ChStart* start;  // shared memory
+  const ChStart start;
   bool later;            // the first piece is still to come
   Request r;
   int b, h, pair, tpt;
   int kb, ke, n0, n1;  // this piece; key blocks of the unit's tiles
   int left, at;        // what is left of the run after this piece; the unit's place in the line
-  __device__ ChWalk(const PagedAttn& params, const ChStart* s, int tokens)
+  __device__ ChWalk(const PagedAttn& params, const ChStart& s, int tokens)
       : p(params), start(s), later(false), tpt(tokens) {
     kb = ke = 0;
-    if (s->count > 0) {
+    if (s.count > 0) {
       begin();
       later = kb > 0;
       if (later || !valid()) next();
     }
   }
   __device__ void begin() {
-    b = start->b;
-    h = start->h;
-    pair = start->pair;
-    left = start->count;
-    at = start->first - start->skip;
+    b = start.b;
+    h = start.h;
+    pair = start.pair;
+    left = start.count;
+    at = start.first - start.skip;
     r = paged_request(p, b, false);
-    take(start->skip);
+    take(start.skip);
   }
   __device__ void take(int skip) {
     n0 = ch_blocks(r, 2 * pair, tpt, p.causal);
@@ -265,7 +246,7 @@ struct ChWalk {
         }
         return;
       }
-      if (++pair == ch_pairs(r, tpt)) {
+      if (++pair == ch_pairs(p, r, tpt)) {
         pair = 0;
         if (++h == p.Hkv) {
           h = 0;
@@ -451,22 +432,16 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
       prefetch_tmap(&tmV);
     }
   }
-  ChStart* start = reinterpret_cast<ChStart*>(bar_gen + 8 * C::BARS + 8);
   pdl_wait();
-  if (warp == 0) {  // not before: the kernel that is waited for may still need tensor memory
-    __syncwarp();
+  if (warp == 2) {  // not before: the kernel that is waited for may still need tensor memory
     tmem_alloc(smem_addr(tmem_slot), 512);
     tmem_relinquish();
   }
-  const ChStart d = ch_start<C::THREADS>(p, tpt, reinterpret_cast<int*>(gen));  // in the Q buffers, not in use yet
-  if (threadIdx.x == 0) *start = d;
-  fence_proxy_async_smem();  // TMA writes there next
+  if (threadIdx.x == 0) reinterpret_cast<PartDesc*>(p.desc)[blockIdx.x].last = -1;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  if (threadIdx.x == 0) reinterpret_cast<PartDesc*>(p.desc)[blockIdx.x].last = -1;
-
   // The m-th unit of the block (a whole warp or one thread); the warp says when it
   // is done with it.
   auto unit_get = [&](uint32_t m, ChUnit& u) -> bool {
@@ -523,7 +498,7 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
           ChUnit u;
           u.b = w.b, u.h = w.h, u.t0 = w.r.t0, u.nq = w.r.nq;
           u.kv = w.r.kv, u.tok0 = 2 * w.pair * tpt, u.kb = w.kb, u.ke = w.ke;
-          u.n0 = w.n0, u.n1 = w.n1, u.whole = w.whole(), u.last = w.valid() ? w.last() / start->per : 0;
+          u.n0 = w.n0, u.n1 = w.n1, u.whole = w.whole(), u.last = w.valid() ? w.last() / w.start.per : 0;
           u.put(sUnit + 64 * (m % kChUnits));
           mbar_arrive(bUFull + 8 * (m % kChUnits));
         }
@@ -531,7 +506,7 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
       if constexpr (!FP8) {
         uint32_t m = 0;
         if (is_k) {
-          ChWalk w(p, start, tpt);
+          ChWalk w(p, ch_start(p, tpt), tpt);
           for (;; w.next(), ++m) {
             publish(w, m);
             if (!ok || !w.valid()) break;
@@ -573,7 +548,7 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
         // block, converts its half of V. The copies run ahead, with a place in
         // the units of their own; block i's slot is free once block i - nslot
         // has been used, which no later block's V is needed for.
-        ChWalk walk(p, start, tpt);  // K warp
+        ChWalk walk(p, is_k ? ch_start(p, tpt) : ChStart{}, tpt);  // K warp
         ChUnit ld, w;
         uint32_t issued = 0, it = 0, lm = 0, m = 0;
         int lj = 0;
@@ -931,7 +906,9 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
       const float inv = !whole ? 1.0f : (l_run == 0.0f ? 0.0f : v_mult / l_run);
       const int hq = w.h * p.G + rhead;
       __nv_bfloat16* orow = p.o + (static_cast<int64_t>(w.t0 + (real ? tok : 0)) * p.Hq + (real ? hq : 0)) * DV;
-      float* prow = p.part_o + (real ? part : 0) * DV;
+      // parts: [slot][DV / 4][row][4], whole lines for a warp's 32 rows
+      float* prow = p.part_o + static_cast<int64_t>(2 * blockIdx.x + (w.kb > 0 ? 0 : 1)) * p.slot_rows * DV +
+                    (real ? t * tpt * p.G + r : 0) * 4;
 #pragma unroll 1
       for (int cc = 0; cc < DV; cc += 32) {
         uint32_t orr[32];
@@ -950,7 +927,7 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
         } else if (real) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<uint4*>(prow + cc + 4 * i) =
+            *reinterpret_cast<uint4*>(prow + static_cast<int64_t>(cc / 4 + i) * p.slot_rows * 4) =
                 make_uint4(orr[4 * i], orr[4 * i + 1], orr[4 * i + 2], orr[4 * i + 3]);
         }
       }
@@ -971,7 +948,7 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
   // -------------------------------------------------------------- teardown
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 2) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);

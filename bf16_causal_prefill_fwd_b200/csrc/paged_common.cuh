@@ -132,6 +132,7 @@ struct PagedAttn {
   const int* kv_lens;  // [B] keys of each request, new ones included
   int B, T, Hq, Hkv, G;
   FastDiv group;  // G
+  FastDiv pair;   // tokens of a pair of row tiles (chunks)
   int num_pages, page_size;
   FastDiv rows;  // page_size
   int box;       // rows of a page one TMA copy takes: gcd(page_size, key tile)
@@ -185,6 +186,71 @@ __device__ __forceinline__ int paged_page(const PagedAttn& p, int b, int key, in
 // Row of its page that key `key` has.
 __device__ __forceinline__ int paged_row(const PagedAttn& p, int key) {
   return key - static_cast<int>(static_cast<uint32_t>(key) / p.rows) * p.page_size;
+}
+
+// A block's run of a line of work that all requests form in order, request b
+// taking cost(b) * Hkv of it: runs are `per` long, this one starts at `first`,
+// `off` into request b, and is `count` long.
+struct Run {
+  int b, off, count, first, per;
+};
+
+// By one whole warp, 32 requests at a time (the next ones' lengths, the only
+// memory it waits for, are read ahead): the sum of the costs in 64 bits --
+// requests whose rows overlap could make the line longer than the host's bound,
+// which is then refused -- and the request the run starts in by a scan over the
+// lanes. No other warp waits meanwhile.
+template <typename Cost>
+__device__ __forceinline__ Run plan_run(const PagedAttn& p, Cost cost) {
+  const int lane = threadIdx.x & 31;
+  const bool report = blockIdx.x == 0;
+  Request ahead = {0, 0, 0};
+  if (lane < p.B) ahead = paged_request(p, lane, report);
+  int c = 0;
+  long long sum = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const Request x = ahead;
+    ahead.nq = 0;
+    if (b0 + 32 + lane < p.B) ahead = paged_request(p, b0 + 32 + lane, report);
+    c = b0 + lane < p.B ? cost(x) : 0;
+    sum += c;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  Run r = {0, 0, 0, 0, 1};
+  if (sum * p.Hkv >= (1ll << 31)) {
+    if (report && lane == 0) paged_report(kPagedInvalid);
+    return r;
+  }
+  const int total = static_cast<int>(sum) * p.Hkv;
+  r.per = (total + gridDim.x - 1) / static_cast<int>(gridDim.x);
+  r.first = blockIdx.x * r.per;
+  r.count = max(0, min(r.per, total - r.first));
+  if (r.count == 0) return r;
+  int before = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    int x = c;  // of 32 requests or fewer
+    if (p.B > 32) x = b0 + lane < p.B ? cost(paged_request(p, b0 + lane, false)) : 0;
+    x *= p.Hkv;
+    int inc = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += u;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, r.first < before + inc);
+    if (past != 0) {
+      const int at = __ffs(past) - 1;
+      r.b = b0 + at;
+      r.off = __shfl_sync(0xffffffffu, r.first - (before + inc - x), at);
+      return r;
+    }
+    before += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  r.count = 0;  // lengths that changed while being read
+  return r;
 }
 
 // The part of a split unit that begins in a block, for the merge: its rows, and

@@ -544,125 +544,4 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<DQK, DV, FP8, NT>::BLOCKS)
   }
 }
 
-// Joins the parts of the units that several blocks have worked on: block c of
-// the grid takes the unit that begins, but does not end, in block c; its rows
-// are spread over gridDim.y. O = sum_b 2^(m_b - M) O_b / sum_b 2^(m_b - M) l_b,
-// the running way, in block order. All it waits for is memory, so (m, l) and O of
-// several parts are asked for at once, neither depending on the other.
-// Few parts (a chunk's unit cut in two or three): 8 lanes take a row, a block 16
-// rows. A row may also have hundreds (one long request over the whole GPU): then
-// a block takes a row, each of its warps every fourth part, and the four results
-// meet in shared memory.
-constexpr int kJoinFew = 8;
-
-struct JoinRow {
-  float m = -INFINITY, l = 0.0f;
-  // Factors of what has been added so far and of the part (x.x, x.y) = (m, l). A
-  // part with l = 0 saw none of the row's keys and may have left O unwritten.
-  __device__ __forceinline__ void add(float2 x, float& keep, float& take) {
-    keep = 1.0f;
-    take = 0.0f;
-    if (x.y == 0.0f) return;
-    const float mn = fmaxf(m, x.x);
-    keep = m == -INFINITY ? 0.0f : ex2_approx(m - mn);
-    take = ex2_approx(x.x - mn);
-    m = mn;
-    l = fmaf(l, keep, x.y * take);
-  }
-};
-
-__device__ __forceinline__ void join_add(float4& acc, const float4& o, float keep, float take) {
-  if (take == 0.0f) return;  // (a NaN factor is not 0)
-  acc.x = fmaf(acc.x, keep, o.x * take);
-  acc.y = fmaf(acc.y, keep, o.y * take);
-  acc.z = fmaf(acc.z, keep, o.z * take);
-  acc.w = fmaf(acc.w, keep, o.w * take);
-}
-
-template <int DV>
-__global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttn p) {
-  static_assert(DV == 128, "8 lanes x 16 or 32 lanes x 4 columns");
-  __shared__ float s_o[4][DV], s_ml[4][2];
-  pdl_launch_dependents();
-  pdl_wait();
-  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const PartDesc e = reinterpret_cast<const PartDesc*>(p.desc)[c];
-  if (e.last < 0) return;
-  const int parts = e.last - c + 1;
-  const float v_scale = p.v_scale != nullptr ? __ldg(p.v_scale + e.hkv) : 1.0f;
-  // part i: the tail slot of the first block, then the head slots of the next ones
-  auto slot = [&](int i) { return static_cast<int64_t>(2 * (c + i) + (i == 0 ? 1 : 0)) * p.slot_rows; };
-  auto place = [&](int r, int& tok, int& hq) {
-    const int row = e.row0 + r;
-    tok = row / p.G;
-    hq = e.hkv * p.G + row - tok * p.G;
-    tok += e.t0;
-  };
-  if (parts <= kJoinFew) {
-    const int l8 = lane & 7;
-    for (int r = 16 * blockIdx.y + 4 * warp + (lane >> 3); r < e.nrows; r += 16 * gridDim.y) {
-      JoinRow j;
-      float4 acc[4] = {};
-#pragma unroll 2
-      for (int i = 0; i < parts; ++i) {
-        const int64_t at = slot(i) + r;
-        const float2 x = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
-        float4 o[4];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) o[n] = *reinterpret_cast<const float4*>(p.part_o + at * DV + 32 * n + 4 * l8);
-        float keep, take;
-        j.add(x, keep, take);
-#pragma unroll
-        for (int n = 0; n < 4; ++n) join_add(acc[n], o[n], keep, take);
-      }
-      int tok, hq;
-      place(r, tok, hq);
-      const float inv = j.l == 0.0f ? 0.0f : v_scale / j.l;
-      __nv_bfloat16* out = p.o + (static_cast<int64_t>(tok) * p.Hq + hq) * DV + 4 * l8;
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-        *reinterpret_cast<uint2*>(out + 32 * n) =
-            make_uint2(pack_bf16x2(acc[n].x * inv, acc[n].y * inv), pack_bf16x2(acc[n].z * inv, acc[n].w * inv));
-      if (p.lse != nullptr && l8 == 0)
-        p.lse[static_cast<int64_t>(hq) * p.T + tok] = j.l == 0.0f ? -INFINITY : (j.m + fast_log2(j.l)) * kLn2;
-    }
-    return;
-  }
-  for (int r = blockIdx.y; r < e.nrows; r += gridDim.y) {
-    JoinRow j;
-    float4 acc = {};
-#pragma unroll 4
-    for (int i = warp; i < parts; i += 4) {
-      const int64_t at = slot(i) + r;
-      const float2 x = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
-      const float4 o = *reinterpret_cast<const float4*>(p.part_o + at * DV + 4 * lane);
-      float keep, take;
-      j.add(x, keep, take);
-      join_add(acc, o, keep, take);
-    }
-    *reinterpret_cast<float4*>(&s_o[warp][4 * lane]) = acc;
-    if (lane == 0) {
-      s_ml[warp][0] = j.m;
-      s_ml[warp][1] = j.l;
-    }
-    __syncthreads();
-    const int td = threadIdx.x;
-    JoinRow all;
-    float sum = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      float keep, take;
-      all.add(make_float2(s_ml[w][0], s_ml[w][1]), keep, take);
-      if (take != 0.0f) sum = fmaf(sum, keep, s_o[w][td] * take);
-    }
-    int tok, hq;
-    place(r, tok, hq);
-    p.o[(static_cast<int64_t>(tok) * p.Hq + hq) * DV + td] =
-        __float2bfloat16(all.l == 0.0f ? 0.0f : sum * (v_scale / all.l));
-    if (p.lse != nullptr && td == 0)
-      p.lse[static_cast<int64_t>(hq) * p.T + tok] = all.l == 0.0f ? -INFINITY : (all.m + fast_log2(all.l)) * kLn2;
-    __syncthreads();  // s_o is written again
-  }
-}
-
 }  // namespace b200p
