@@ -170,6 +170,14 @@ at::Tensor empty(c10::IntArrayRef shape, at::ScalarType dtype, const c10::Device
   return at::empty(shape, c10::TensorOptions().dtype(dtype).device(dev));
 }
 
+// n elements of a 1-D tensor from `at` on, in its storage.
+at::Tensor part(const at::Tensor& of, int64_t at, int64_t n) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(of.storage()), of.key_set(), of.dtype());
+  t.unsafeGetTensorImpl()->set_storage_offset(at);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+  return t;
+}
+
 // The tensors' device as the current one for the call, and the stream to launch on.
 struct Launch {
   c10::cuda::OptionalCUDAGuard guard;
@@ -227,9 +235,11 @@ PyObject* slots(PyObject*, PyObject* const* a, Py_ssize_t n) {
     } else if (given(a[6]) || given(a[7])) {
       throw Refused("free_head goes with free_pages");
     }
-    at::Tensor cu = empty({B + 1}, at::kInt, dev), kv = empty({B}, at::kInt, dev);
-    at::Tensor pos = empty({total}, at::kInt, dev), slot = empty({total}, at::kInt, dev);
-    if (free && !head_out.defined()) head_out = empty({1}, at::kInt, dev);
+    // one allocation: cu_seqlens, kv_lens, positions, slots, head
+    const at::Tensor all = empty({2 * B + 2 + 2 * static_cast<int64_t>(total)}, at::kInt, dev);
+    at::Tensor cu = part(all, 0, B + 1), kv = part(all, B + 1, B);
+    at::Tensor pos = part(all, 2 * B + 1, total), slot = part(all, 2 * B + 1 + total, total);
+    if (free && !head_out.defined()) head_out = part(all, 2 * B + 1 + 2 * static_cast<int64_t>(total), 1);
     Launch l(dev, a[8]);
     const int rc = fn_slots(table.ptr, table.row, table.width, static_cast<const int*>(ctx.data_ptr()),
                             static_cast<const int*>(nw.data_ptr()), int32(B, "batch"), total, ps, free, count, head,
