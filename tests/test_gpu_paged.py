@@ -280,6 +280,22 @@ def test_append_of_special_values_into_e4m3():
     assert torch.equal(kc.view(torch.uint8), vc.view(torch.uint8))
 
 
+def test_append_codes_of_every_bf16_value():
+    """Bytes, the sign of zero included, from scales of both kinds of division."""
+    scales = torch.tensor([1.0, 0.0078, 3.0, 1 / 3, 2.0 ** -60, 1.7e-30, 4.4e31, 0.02373])
+    x = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).view(512, 1, 128).expand(-1, 8, -1).contiguous()
+    want = plain_codes(x, scales)
+    kc, vc = (torch.zeros(32, 16, 8, 128, dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2))
+    sc = scales.cuda()
+    b2.paged_append_kv(x.cuda(), x.cuda(), kc, vc, ints(list(range(512))), k_scale=sc, v_scale=sc)
+    assert b2.check() == 0
+    number = ~x.float().isnan()
+    for c in (kc, vc):
+        got = c.cpu().view(512, 8, 128)
+        assert torch.equal(got.view(torch.uint8)[number], want.view(torch.uint8)[number])
+        assert bool(got.float()[~number].isnan().all())
+
+
 def test_append_slots_past_the_cache_are_skipped_and_reported():
     kc, vc = (torch.zeros(2, 16, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
     x = torch.ones(3, 2, 128, dtype=torch.bfloat16, device="cuda")
