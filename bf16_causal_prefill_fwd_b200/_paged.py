@@ -2,7 +2,7 @@
 
 A cache is two tensors, k_cache [pages, page_size, Hkv, d_qk] and v_cache
 [pages, page_size, Hkv, d_v], bf16 or e4m3 (torch.float8_e4m3fn or uint8 codes)
-with one fp32 scale per key/value head. They may be views (a [pages, Hkv,
+with one positive fp32 scale per key/value head. They may be views (a [pages, Hkv,
 page_size, d] buffer permuted, K and V halves of one buffer): rows of d elements
 are contiguous, the other strides are multiples of 16 bytes.
 

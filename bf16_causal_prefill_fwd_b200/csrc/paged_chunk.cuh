@@ -38,7 +38,12 @@
 // takes 395 (4 requests of 500-1300 new tokens, 2-12k keys).
 //
 // Bound by the tensor core (2 x 2 x 128^3 products per key block and pair) and,
-// for chunks of a few tokens, by reading the cache.
+// for chunks of a few tokens, by reading the cache. Measured: 4096 tokens over 32k
+// keys (32/8 heads of 128, bf16) 1.73-1.85 ms, 1110-1190 TFLOP/s under the power cap,
+// tensor pipe 70% busy; ragged chunks of 1-1500 tokens 175-208 us (45%: each SM's
+// run begins with an empty pipeline and ends with a part to write and join); the same
+// kind over an e4m3 cache 360-415 us; 192/128 heads 217-257 us (55%); 32 requests
+// of 3-9 drafted tokens 115-138 us, 4.7-5.6 TB/s of cache.
 #pragma once
 
 #include "paged_common.cuh"

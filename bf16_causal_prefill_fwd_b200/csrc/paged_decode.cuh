@@ -26,6 +26,12 @@
 // operand with movmatrix; O^T = V^T P^T. The tensor cores' own rate is of no
 // concern here: 16 products per 8 KB of cache.
 //
+// Measured (G = 4, Hkv = 8, d = 128): 64 requests of up to 16k keys, bf16, 1.88 GB
+// of cache: 282 us, 6.6 TB/s, what a plain copy reaches; 24 requests of 9-32k keys,
+// e4m3, 1.0 GB: 171 us, 5.8 TB/s, held back by the conversions (30% of the issue
+// slots in bursts between the products); one request of 4096 keys: 9.1 us, of which
+// two launches and the join are about 6.
+//
 // e4m3 caches: codes become fp16 exactly (cvt.rn.f16x2.e4m3x2), Q is brought to
 // fp16 by a power of two per row (its largest element in [1/2, 1): every bf16
 // above 2^-16 of it keeps all its bits), P is fp16; the scales of K and V go

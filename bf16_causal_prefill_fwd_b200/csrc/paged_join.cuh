@@ -2,8 +2,9 @@
 // the grid takes the unit that begins, but does not end, in block c; its rows
 // are spread over gridDim.y. O = sum_b 2^(m_b - M) O_b / sum_b 2^(m_b - M) l_b,
 // the running way, in block order, so results do not depend on timing. All it
-// waits for is memory, so (m, l) and O of several parts are asked for at once,
-// neither depending on the other.
+// waits for is memory (2 to 5 us behind the attention kernel, most of it the
+// launch), so (m, l) and O of several parts are asked for at once, neither
+// depending on the other.
 #pragma once
 
 #include "paged_common.cuh"

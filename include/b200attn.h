@@ -359,9 +359,10 @@ int b200attn_quantize_fp8_static(const void* x, void* x_fp8, float* scale,
  * and are reported by the next b200attn_check.
  */
 
-/* A paged cache. Strides are in elements, multiples of 16 bytes; the d elements
- * of a row are contiguous, so [pages, page_size, Hkv, d], [pages, Hkv, page_size,
- * d] and K and V interleaved in one tensor are all described. */
+/* A paged cache. Strides are in elements, positive and multiples of 16 bytes; the
+ * d elements of a row are contiguous and rows do not overlap, so [pages, page_size,
+ * Hkv, d], [pages, Hkv, page_size, d] and K and V interleaved in one tensor are all
+ * described. */
 typedef struct {
   void* k;  /* bf16, or e4m3 codes */
   void* v;
@@ -372,7 +373,7 @@ typedef struct {
   int Hkv;
   int d_qk, d_v;  /* (128, 128) or (192, 128) */
   int dtype;      /* B200ATTN_BF16 or B200ATTN_FP8_E4M3 */
-  const float* k_scale; /* e4m3: device fp32 [Hkv]; a code c stands for decode(c) * scale */
+  const float* k_scale; /* e4m3: device fp32 [Hkv], > 0; a code c stands for decode(c) * scale */
   const float* v_scale;
 } b200attn_paged_cache;
 
@@ -449,16 +450,18 @@ size_t b200attn_paged_fwd_workspace_bytes(int total, int max_seqlen_q, int Hq, i
  * q      bf16 [total, Hq, d_qk], tokens q_stride elements apart (a multiple of
  *        8), a token's heads contiguous; Hq / Hkv <= 128; query head h uses
  *        key/value head h / (Hq / Hkv)
- * cache  bf16: products in bf16, fp32 accumulation. e4m3: codes are taken as
- *        fp16 exactly, Q and the probabilities as fp16 (Q after an exact power
- *        of two per row), fp32 accumulation, per-head scales.
+ * cache  bf16: products in bf16, fp32 accumulation. e4m3: codes are taken
+ *        exactly, Q after a power of two per row as fp16 or as the sum of two e4m3
+ *        numbers (what is 2^-10 of the row's largest element or more keeps all its
+ *        bits), the probabilities as fp16; fp32 accumulation, per-head scales.
  * block_table  int32 [batch, table_width], rows table_stride apart. Only the
  *        entries of the first kv_lens[b] rows are read. An entry that is no page
  *        reads as zero keys and values, and INVALID is reported.
  * cu_seqlens  int32 [batch + 1]: new tokens [cu[b], cu[b+1]) belong to request b.
  *        Rows of o and lse in no request (padding behind the last) stay as they
  *        are.
- * kv_lens  int32 [batch]: keys of each request, the new tokens' included
+ * kv_lens  int32 [batch]: keys of each request, the new tokens' included;
+ *        table_width * page_size < 2^30
  * total  rows of q and o
  * max_seqlen_q  upper bound on the new tokens of any request, known on the host
  *        (`total` if nothing better is); a request with more is skipped and
@@ -468,11 +471,13 @@ size_t b200attn_paged_fwd_workspace_bytes(int total, int max_seqlen_q, int Hq, i
  * softmax_scale  s; a value <= 0 selects 1/sqrt(d_qk)
  * workspace  b200attn_paged_fwd_workspace_bytes bytes, 16-byte aligned, contents
  *        on entry irrelevant; calls that may overlap (on different streams, in
- *        different graphs) need distinct ones
+ *        different graphs) need distinct ones. What a captured call was given
+ *        has to live as long as its graph.
  *
  * Cache rows at or behind kv_lens[b] are never part of a result, whatever they
- * hold (NaN included). Results do not depend on timing: the same contents give
- * the same bytes.
+ * hold (NaN included). A NaN or infinite value among a request's own keys reaches
+ * the rows that see it, and may reach those whose causal mask hides it. Results
+ * do not depend on timing: the same contents give the same bytes.
  *
  * Errors: INVALID, UNSUPPORTED (head dims, page_size not a multiple of 16,
  * Hq / Hkv > 128, sizes past 32-bit counts), WORKSPACE, CUDA.
@@ -485,7 +490,7 @@ int b200attn_paged_fwd(const void* q, size_t q_stride, const b200attn_paged_cach
 
 /*
  * b200attn_check -- synchronise `stream`, then return and clear the device
- * status word: 0, or B200ATTN_ERR_TIMEOUT if any kernel of this library gave
+ * status words: 0, or B200ATTN_ERR_TIMEOUT if any kernel of this library gave
  * up on a wait since the last check, or what a call found in its inputs on the
  * device (INVALID, PAGES); B200ATTN_ERR_CUDA if synchronising fails.
  */

@@ -108,8 +108,8 @@ def check_attention(p: Paged, got, lse=None, causal=True, softmax_scale=None):
     d = p.q.shape[2]
     half = HALF_STEP[torch.float16 if p.k_scale is not None else torch.bfloat16]
     score = (d + 2) * 2.0 ** -24 * reach + 2.0 ** -22 + 2.2e-4      # [Hq, T]
-    # fp16 probabilities below 2^-14 are off by 2^-25 at most, relative to a largest one of at least 2^-10
-    tiny = 2.0 ** -15 * 0 + p.kv_lens.max().item() * 2.0 ** -15 * 2.0 ** -10 * (p.k_scale is not None)
+    # fp16 probabilities below 2^-14 are off by 2^-25 at most, beside a largest one of at least 1
+    tiny = p.kv_lens.max().item() * 2.0 ** -25 * (p.k_scale is not None)
     bound = a * (half + 2 * score.T[..., None]) + a.amax(-1, keepdim=True).clamp(min=1.0) * tiny + o.abs() * 2.0 ** -8 + 1e-30
     real = ~o.isnan()
     got = got.double().cpu()
