@@ -382,7 +382,7 @@ int b200attn_paged_fwd(const void* q, size_t q_stride, const b200attn_paged_cach
   if (Hq % cache->Hkv != 0 || (causal != 0 && causal != 1) || !std::isfinite(softmax_scale)) return B200ATTN_ERR_INVALID;
   if (total == 0) return B200ATTN_OK;  // no new tokens
   if (!q || !o || !block_table || !cu_seqlens || !kv_lens) return B200ATTN_ERR_INVALID;
-  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(block_table, 4) || !aligned(cu_seqlens, 4) ||
+  if (!aligned(q, 16) || !aligned(o, 32) || !aligned(block_table, 4) || !aligned(cu_seqlens, 4) ||
       !aligned(kv_lens, 4) || !aligned(lse, 4) || !rows_ok(q_stride, total, Hq, cache->d_qk))
     return B200ATTN_ERR_INVALID;
   const int G = Hq / cache->Hkv;

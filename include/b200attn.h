@@ -466,7 +466,7 @@ size_t b200attn_paged_fwd_workspace_bytes(int total, int max_seqlen_q, int Hq, i
  * max_seqlen_q  upper bound on the new tokens of any request, known on the host
  *        (`total` if nothing better is); a request with more is skipped and
  *        INVALID reported, like one whose cu_seqlens or kv_lens do not fit
- * o      bf16 [total, Hq, d_v], contiguous
+ * o      bf16 [total, Hq, d_v], contiguous, 32-byte aligned
  * lse    optional fp32 [Hq, total]
  * softmax_scale  s; a value <= 0 selects 1/sqrt(d_qk)
  * workspace  b200attn_paged_fwd_workspace_bytes bytes, 16-byte aligned, contents

@@ -210,6 +210,7 @@ def test_attn_entry_point_refuses(real):
     assert c_attn(real, cache(), total=1 << 28, hq=HQ) == -2          # rows past 32-bit counts
     assert c_attn(real, cache(), ws=None) == -5
     assert c_attn(real, cache(), wsb=64) == -5
+    assert c_attn(real, cache(), o=FAKE + 16) == -1                    # rows leave in stores of 32 bytes
     assert c_attn(real, cache(), ws=FAKE + 4) == -5
     assert c_attn(real, cache(), total=0, q=None, o=None) == 0        # nothing to do
 
