@@ -306,22 +306,6 @@ struct ChUnit {
   }
 };
 
-// 2^x for two lanes on the FMA pipe (Cody-Waite split, degree-3 polynomial of
-// relative error 2.2e-4 on [-1/2, 1/2]); below -125: 0.
-__device__ __forceinline__ void ch_exp2_fma(float x0, float x1, float& r0, float& r1) {
-  constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
-  const float a0 = fmaxf(x0, -125.0f), a1 = fmaxf(x1, -125.0f);
-  float j0, j1, n0, n1, f0, f1, p0, p1;
-  ffma2_bcast(a0, a1, 1.0f, kRound, j0, j1);
-  ffma2_bcast(j0, j1, 1.0f, -kRound, n0, n1);
-  ffma2(n0, n1, -1.0f, -1.0f, a0, a1, f0, f1);
-  ffma2_bcast(f0, f1, 0.05286737531423569f, 0.24215202033519745f, p0, p1);
-  ffma2(p0, p1, f0, f1, 0.6935867667198181f, 0.6935867667198181f, p0, p1);
-  ffma2(p0, p1, f0, f1, 0.9999627470970154f, 0.9999627470970154f, p0, p1);
-  r0 = x0 >= -125.0f ? __uint_as_float(__float_as_uint(p0) + (__float_as_uint(j0) << 23)) : 0.0f;
-  r1 = x1 >= -125.0f ? __uint_as_float(__float_as_uint(p1) + (__float_as_uint(j1) << 23)) : 0.0f;
-}
-
 __device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
@@ -868,23 +852,18 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
         }
         l_run *= alpha;
 
-        // probabilities, packed in place; a row that has seen nothing yet has m = -inf and only masked scores
+        // probabilities, packed in place; a row that has seen nothing yet has m = -inf and only masked scores.
+        // All on the MUFU unit: what these warps lack is issue slots (and, under the power cap, energy), and a
+        // polynomial for one score in four on the FMA pipe took long chunks 1765 us for 1690, e4m3 chunks 403 for
+        // 362; for one in eight 1727 and 393.
         const float nm = m_run == -INFINITY ? 0.0f : -m_run;
         float sa = 0.f, sb = 0.f, sc = 0.f, sd = 0.f;
 #pragma unroll
         for (int c = 0; c < 128; c += 4) {
-          float y0, y1, y2, y3, p0, p1, p2, p3;
+          float y0, y1, y2, y3;
           ffma2_bcast(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]), c_log2, nm, y0, y1);
           ffma2_bcast(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]), c_log2, nm, y2, y3);
-          if ((c & 12) == 12) {  // one score in four off the MUFU unit
-            ch_exp2_fma(y0, y1, p0, p1);
-            ch_exp2_fma(y2, y3, p2, p3);
-          } else {
-            p0 = ex2_approx(y0);
-            p1 = ex2_approx(y1);
-            p2 = ex2_approx(y2);
-            p3 = ex2_approx(y3);
-          }
+          const float p0 = ex2_approx(y0), p1 = ex2_approx(y1), p2 = ex2_approx(y2), p3 = ex2_approx(y3);
           fadd2(sa, sb, p0, p1);
           fadd2(sc, sd, p2, p3);
           sr[c >> 1] = FP8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);

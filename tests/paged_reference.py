@@ -102,12 +102,12 @@ def attention(p: Paged, causal=True, softmax_scale=None):
 def check_attention(p: Paged, got, lse=None, causal=True, softmax_scale=None):
     """Elementwise bounds. A probability carries the half step of its 16-bit type and an exponential of fp32 scores:
     an fp32 sum of d products is off by at most (d + 2) 2^-24 sum |q_d k_d|, which is a relative error of the
-    probability; so are the base-2 exponential's 2^-22 and, for bf16, the prefill kernels' polynomial's 2.2e-4. Each
-    probability enters numerator and sum, and the output is rounded to bf16 once."""
+    probability; so is the base-2 exponential's 2^-22. Each probability enters numerator and sum, and the output is
+    rounded to bf16 once."""
     o, ref_lse, a, reach = attention(p, causal, softmax_scale)
     d = p.q.shape[2]
     half = HALF_STEP[torch.float16 if p.k_scale is not None else torch.bfloat16]
-    score = (d + 2) * 2.0 ** -24 * reach + 2.0 ** -22 + 2.2e-4      # [Hq, T]
+    score = (d + 2) * 2.0 ** -24 * reach + 2.0 ** -22      # [Hq, T]
     # fp16 probabilities below 2^-14 are off by 2^-25 at most, beside a largest one of at least 1
     tiny = p.kv_lens.max().item() * 2.0 ** -25 * (p.k_scale is not None)
     bound = a * (half + 2 * score.T[..., None]) + a.amax(-1, keepdim=True).clamp(min=1.0) * tiny + o.abs() * 2.0 ** -8 + 1e-30
