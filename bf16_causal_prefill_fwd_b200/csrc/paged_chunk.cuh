@@ -340,28 +340,27 @@ __device__ __forceinline__ void st_global_32b(void* p, const uint32_t* v) {
 }
 
 // Rows [64 half, 64 half + 64) of a staged 128 x 128 block of V's codes -> the
-// fp16 tile, by one warp; rows from `keys` on as zeros.
-__device__ __forceinline__ void ch_convert_v(const uint4* staged, uint32_t dst, int half, int lane, int keys) {
-  const int u = lane & 7;           // 16 codes of a row: columns 16 u ..
-  const bool odd = (u >> 2) & 1;    // second column block: its units go out in the opposite order,
-  const int u0 = 2 * (u & 3) + (odd ? 1 : 0);  // so that eight lanes of a row hit all eight 16-byte banks
-  const uint32_t col = dst + (u >> 2) * (kChN * 128);
+// fp16 tile, by one warp; rows from `keys` on as zeros. 16 lanes take a row, eight
+// codes each: eight lanes' stores are one row of a column block, all 32 banks.
+__device__ __forceinline__ void ch_convert_v(const uint2* staged, uint32_t dst, int half, int lane, int keys) {
+  const int u = lane & 7;
+  const uint32_t col = dst + ((lane >> 3) & 1) * (kChN * 128);
 #pragma unroll 1
-  for (int g = 0; g < 4; ++g) {
-    uint4 c[4];
+  for (int g = 0; g < 8; ++g) {
+    uint2 c[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = staged[(64 * half + 16 * g) * 8 + 32 * i + lane];
+    for (int i = 0; i < 4; ++i) c[i] = staged[(64 * half + 8 * g) * 16 + 32 * i + lane];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int row = 64 * half + 16 * g + 4 * i + (lane >> 3);
-      const uint4 v = row < keys ? c[i] : make_uint4(0u, 0u, 0u, 0u);
-      const uint32_t line = col + row * 128;
-      const uint32_t x0 = odd ? v.z : v.x, x1 = odd ? v.w : v.y, y0 = odd ? v.x : v.z, y1 = odd ? v.y : v.w;
-      st_shared_v4(line + ((u0 ^ (row & 7)) << 4), e4m3x2_f16x2(x0), e4m3x2_f16x2(x0 >> 16), e4m3x2_f16x2(x1),
-                   e4m3x2_f16x2(x1 >> 16));
-      st_shared_v4(line + (((u0 ^ 1) ^ (row & 7)) << 4), e4m3x2_f16x2(y0), e4m3x2_f16x2(y0 >> 16), e4m3x2_f16x2(y1),
-                   e4m3x2_f16x2(y1 >> 16));
+      const int row = 64 * half + 8 * g + 2 * i + (lane >> 4);
+      st_shared_v4(col + row * 128 + ((u ^ (row & 7)) << 4), e4m3x2_f16x2(c[i].x), e4m3x2_f16x2(c[i].x >> 16),
+                   e4m3x2_f16x2(c[i].y), e4m3x2_f16x2(c[i].y >> 16));
     }
+  }
+  if (keys < 64 * half + 64) {  // whatever they were converted from
+    __syncwarp();
+    for (int row = max(keys, 64 * half) + (lane >> 4); row < 64 * half + 64; row += 2)
+      st_shared_v4(col + row * 128 + ((u ^ (row & 7)) << 4), 0u, 0u, 0u, 0u);
   }
 }
 
@@ -590,7 +589,7 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
             if (ok && it >= C::SV) ok = paged_wait(bVEmpty + 8 * s, ((it / C::SV) - 1) & 1, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            ch_convert_v(reinterpret_cast<const uint4*>(gen + (sVc - base) + cs * C::VC_BYTES), sV + s * C::V_BYTES,
+            ch_convert_v(reinterpret_cast<const uint2*>(gen + (sVc - base) + cs * C::VC_BYTES), sV + s * C::V_BYTES,
                          is_k ? 0 : 1, lane, w.kv - j * kChN);
             fence_proxy_async_smem();
             mbar_arrive(bCEmpty + 8 * cs);
