@@ -56,8 +56,9 @@ constexpr int kChRows = 2 * kChM;
 // What a unit costs beyond its key blocks (its Q, the pipeline's filling, its
 // output), in key blocks: counted in when the line is cut, so that a run of many
 // short units is not longer than one of few long ones. Measured on ragged chunks
-// of 1-1500 tokens and on one 2048-token prompt: 1 block 228 and 88 us, 2 210 and
-// 81, 3 200 and 74, 4 200 and 75, 6 195 and 77.
+// of 1-1500 tokens and on one 2048-token prompt: 2 blocks 185 and 50.8 us, 3 186
+// and 49.9, 4 188 and 50.4, 5 189 and 50.3; a first form of the kernel, slower at
+// a unit's ends, took 228 and 88 us with 1 for 200 and 74 with 3.
 constexpr int kChUnitCost = 3;
 constexpr int kChMaxBlocks = 160;  // workspace slots are sized for this many blocks
 
@@ -174,16 +175,17 @@ __device__ __forceinline__ void ld_shared_v4(uint32_t addr, int& a, int& b, int&
 // `first` is its place in the line; runs are `per` long.
 struct ChStart {
   int b, h, pair, skip, count, first, per;
+  Request r;
 };
 
 // By one warp of the block.
 __device__ __forceinline__ ChStart ch_start(const PagedAttn& p, int tpt) {
   const int lane = threadIdx.x & 31;
   const Run run = plan_run(p, [&](const Request& x) { return ch_head_cost(p, x, tpt); });
-  ChStart d = {run.b, 0, 0, 0, run.count, run.first, run.per};
+  ChStart d = {run.b, 0, 0, 0, run.count, run.first, run.per, run.req};
   if (run.count == 0) return d;
-  const Request r = paged_request(p, run.b, false);
-  const int n = max(1, ch_head_cost(p, r, tpt)), pairs = ch_pairs(p, r, tpt);
+  const Request r = run.req;
+  const int n = max(1, run.cost), pairs = ch_pairs(p, r, tpt);
   d.h = run.off / n;
   int off = run.off - d.h * n;
   for (int i0 = 0; i0 < pairs; i0 += 32) {  // the pair that `off` lies in, 32 at a time
@@ -237,7 +239,7 @@ struct ChWalk {
     pair = start.pair;
     left = start.count;
     at = start.first - start.skip;
-    r = paged_request(p, b, false);
+    r = start.r;
     take(start.skip);
   }
   __device__ void take(int skip) {

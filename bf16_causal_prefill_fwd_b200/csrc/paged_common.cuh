@@ -190,9 +190,10 @@ __device__ __forceinline__ int paged_row(const PagedAttn& p, int key) {
 
 // A block's run of a line of work that all requests form in order, request b
 // taking cost(b) * Hkv of it: runs are `per` long, this one starts at `first`,
-// `off` into request b, and is `count` long.
+// `off` into request b (`req`, of cost `cost` per head), and is `count` long.
 struct Run {
-  int b, off, count, first, per;
+  int b, off, count, first, per, cost;
+  Request req;
 };
 
 // By one whole warp, 32 requests at a time (the next ones' lengths, the only
@@ -208,9 +209,10 @@ __device__ __forceinline__ Run plan_run(const PagedAttn& p, Cost cost) {
   if (lane < p.B) ahead = paged_request(p, lane, report);
   int c = 0;
   long long sum = 0;
+  Request x = {0, 0, 0};
 #pragma unroll 1
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const Request x = ahead;
+    x = ahead;
     ahead.nq = 0;
     if (b0 + 32 + lane < p.B) ahead = paged_request(p, b0 + 32 + lane, report);
     c = b0 + lane < p.B ? cost(x) : 0;
@@ -218,7 +220,7 @@ __device__ __forceinline__ Run plan_run(const PagedAttn& p, Cost cost) {
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  Run r = {0, 0, 0, 0, 1};
+  Run r = {0, 0, 0, 0, 1, 1, {0, 0, 0}};
   if (sum * p.Hkv >= (1ll << 31)) {
     if (report && lane == 0) paged_report(kPagedInvalid);
     return r;
@@ -231,10 +233,15 @@ __device__ __forceinline__ Run plan_run(const PagedAttn& p, Cost cost) {
   int before = 0;
 #pragma unroll 1
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    int x = c;  // of 32 requests or fewer
-    if (p.B > 32) x = b0 + lane < p.B ? cost(paged_request(p, b0 + lane, false)) : 0;
-    x *= p.Hkv;
-    int inc = x;
+    if (p.B > 32) {  // else both are there still
+      c = 0;
+      if (b0 + lane < p.B) {
+        x = paged_request(p, b0 + lane, false);
+        c = cost(x);
+      }
+    }
+    const int y = c * p.Hkv;
+    int inc = y;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, inc, o);
@@ -244,7 +251,11 @@ __device__ __forceinline__ Run plan_run(const PagedAttn& p, Cost cost) {
     if (past != 0) {
       const int at = __ffs(past) - 1;
       r.b = b0 + at;
-      r.off = __shfl_sync(0xffffffffu, r.first - (before + inc - x), at);
+      r.off = __shfl_sync(0xffffffffu, r.first - (before + inc - y), at);
+      r.cost = __shfl_sync(0xffffffffu, c, at);
+      r.req.t0 = __shfl_sync(0xffffffffu, x.t0, at);
+      r.req.nq = __shfl_sync(0xffffffffu, x.nq, at);
+      r.req.kv = __shfl_sync(0xffffffffu, x.kv, at);
       return r;
     }
     before += __shfl_sync(0xffffffffu, inc, 31);
