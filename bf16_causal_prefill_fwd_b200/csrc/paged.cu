@@ -190,7 +190,10 @@ Parts parts_of(int blocks, int rows) {
 }
 
 // The few-rows kernel serves up to 16 query rows per key/value head; the choice
-// is by the bound on a request's new tokens alone, which the host knows.
+// is by the bound on a request's new tokens alone, which the host knows. At 16 rows
+// (4 tokens, 4 heads a group) 64 requests over up to 16k bf16 keys take 323 us with
+// it and 377 with the other, one over 4096 16.4 and 21.1; 24 requests of 12 rows over
+// 9-32k e4m3 keys 199 and 329. Above, its rows would no longer fit the registers.
 bool few_rows(int max_q, int G) { return static_cast<int64_t>(max_q) * G <= b200p::kDecMaxRows; }
 
 template <int DQK, bool FP8, int NT>

@@ -35,15 +35,15 @@
 // would need the same split in the softmax, the busiest warps here; instead V's
 // codes become fp16 (exactly) in shared memory, by the two copying warps, and P
 // is fp16. Converting K as well, with four more warps, took 503 us where this
-// takes 395 (4 requests of 500-1300 new tokens, 2-12k keys).
+// took 395 then (4 requests of 500-1300 new tokens, 2-12k keys).
 //
 // Bound by the tensor core (2 x 2 x 128^3 products per key block and pair) and,
 // for chunks of a few tokens, by reading the cache. Measured: 4096 tokens over 32k
-// keys (32/8 heads of 128, bf16) 1.73-1.85 ms, 1110-1190 TFLOP/s under the power cap,
-// tensor pipe 70% busy; ragged chunks of 1-1500 tokens 175-208 us (45%: each SM's
-// run begins with an empty pipeline and ends with a part to write and join); the same
-// kind over an e4m3 cache 360-415 us; 192/128 heads 217-257 us (55%); 32 requests
-// of 3-9 drafted tokens 115-138 us, 4.7-5.6 TB/s of cache.
+// keys (32/8 heads of 128, bf16) 1.65-1.69 ms, 1220-1250 TFLOP/s under the power cap,
+// tensor pipe 77% busy, MUFU 80%; ragged chunks of 1-1500 tokens 168-187 us (55%: each
+// SM's run begins with an empty pipeline and ends with a part to write and join); the
+// same kind over an e4m3 cache 351-363 us (51%); 192/128 heads 214-249 us (58%); 32
+// requests of 3-9 drafted tokens 117-135 us, 4.8-5.5 TB/s of cache.
 #pragma once
 
 #include "paged_common.cuh"

@@ -27,8 +27,8 @@
 // concern here: 16 products per 8 KB of cache.
 //
 // Measured (G = 4, Hkv = 8, d = 128): 64 requests of up to 16k keys, bf16, 1.88 GB
-// of cache: 282 us, 6.6 TB/s, what a plain copy reaches; 24 requests of 9-32k keys,
-// e4m3, 1.0 GB: 171 us, 5.8 TB/s, held back by the conversions (30% of the issue
+// of cache: 280 us, 6.7 TB/s, what a plain copy reaches; 24 requests of 9-32k keys,
+// e4m3, 1.0 GB: 170 us, 5.9 TB/s, held back by the conversions (30% of the issue
 // slots in bursts between the products); one request of 4096 keys: 9.1 us, of which
 // two launches and the join are about 6.
 //
