@@ -95,7 +95,8 @@ def attn_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, *, max
     kv_lens [B] counts its keys, the new tokens' own included (append them first). With ``causal`` new token i of nq
     sees the keys j <= kv_len - nq + i. ``max_seqlen_q`` bounds the new tokens of any request (default: total); with
     at most 16 / (Hq / Hkv) of them the decoding kernel runs. Returns bf16 [total, Hq, d_v] (and fp32 lse
-    [Hq, total]); rows of no request are left unwritten.
+    [Hq, total]); rows of no request are left unwritten. ``out``, if given,
+    is contiguous and 32-byte aligned.
     """
     r = (_native or _load()).fwd(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, max_seqlen_q, causal, softmax_scale,
                                  k_scale, v_scale, out, return_lse, workspace, _stream(stream))

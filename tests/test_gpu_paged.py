@@ -84,6 +84,21 @@ CHUNK_LENS = [
 ]
 
 
+@pytest.mark.parametrize("B", [32, 33, 64, 91])
+def test_chunks_of_many_requests(B):
+    """More requests than a warp's lanes, some without new tokens: runs begin in any of them."""
+    q_lens = [(5 * i + 3) % 29 if i % 6 else 0 for i in range(B)]
+    p = make(q_lens, [n + (37 * i) % 201 for i, n in enumerate(q_lens)], 8, 2, 128, 16, seed=B)
+    o, lse = run(p)
+    check_attention(p, o, lse)
+
+
+def test_chunk_of_groups_that_are_no_power_of_two():
+    p = make([150, 260], [700, 260], 14, 2, 128, 16, seed=41)   # 18 tokens a row tile, the line's length by Euclid's steps
+    o, lse = run(p)
+    check_attention(p, o, lse)
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("heads", SHAPES)
 @pytest.mark.parametrize("lens", CHUNK_LENS)
