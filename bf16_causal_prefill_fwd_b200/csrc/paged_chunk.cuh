@@ -68,8 +68,10 @@ template <int DQK, int DV, bool FP8>
 struct ChCfg {
   static constexpr int THREADS = 384, REGS_LAUNCH = 168;
   // Register split by warpgroup: copies and issue, softmax; the sum stays within
-  // what the block was launched with.
-  static constexpr int REGS_CTRL = FP8 ? 104 : 72, REGS_SOFT = FP8 ? 200 : 208;
+  // what the block was launched with. The warps that convert V need more, for the
+  // copies' places at 192 most (e4m3 chunks of 128 and 192/128: 88 and 208 registers
+  // 352 and 258 us, 104 and 200 360 and 250, 120 and 192 372 and 252).
+  static constexpr int REGS_CTRL = FP8 ? (DQK == 128 ? 88 : 104) : 72, REGS_SOFT = FP8 && DQK != 128 ? 200 : 208;
   static_assert(128 * REGS_CTRL + 256 * REGS_SOFT <= THREADS * REGS_LAUNCH, "registers");
   static constexpr int CHUNK = kChM * 128;  // 128 rows x 128 bytes, swizzled
   static constexpr int KSZ = FP8 ? 1 : 2;
