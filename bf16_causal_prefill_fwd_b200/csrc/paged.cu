@@ -396,6 +396,12 @@ int b200attn_paged_fwd(const void* q, size_t q_stride, const b200attn_paged_cach
       static_cast<int64_t>(total) * Hq >= (int64_t(1) << 31) ||
       static_cast<int64_t>(batch) * cache->Hkv * (keys / 64 /* the smallest tile */ + 1) >= (int64_t(1) << 31))
     return B200ATTN_ERR_UNSUPPORTED;
+  if (!few_rows(max_seqlen_q, G)) {  // so is the line of key blocks of all pairs of row tiles
+    const int64_t per = 2 * (b200p::kChM / G), most = max_seqlen_q < total ? max_seqlen_q : total;
+    const int64_t each = batch * ((most + per - 1) / per), packed = total / per + batch;
+    if ((each < packed ? each : packed) * cache->Hkv * (keys / b200p::kChN + 1 + b200p::kChUnitCost) >= (int64_t(1) << 31))
+      return B200ATTN_ERR_UNSUPPORTED;
+  }
   const size_t need = b200attn_paged_fwd_workspace_bytes(total, max_seqlen_q, Hq, cache->Hkv);
   if (!workspace || workspace_bytes < need || !aligned(workspace, 16)) return B200ATTN_ERR_WORKSPACE;
   int sm_count = 0, device = 0;

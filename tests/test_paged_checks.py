@@ -208,6 +208,7 @@ def test_attn_entry_point_refuses(real):
     assert c_attn(real, cache(h=1), hq=129, stride=129 * D) == -2                     # a group of more than 128 heads
     assert c_attn(real, cache(), width=(1 << 27) + 1) == -2           # keys past 32-bit counts
     assert c_attn(real, cache(), total=1 << 28, hq=HQ) == -2          # rows past 32-bit counts
+    assert c_attn(real, cache(h=1, token=D), hq=128, stride=128 * D, total=1 << 20, maxq=1 << 20, width=1 << 17) == -2  # the line of work, too
     assert c_attn(real, cache(), ws=None) == -5
     assert c_attn(real, cache(), wsb=64) == -5
     assert c_attn(real, cache(), o=FAKE + 16) == -1                    # rows leave in stores of 32 bytes
