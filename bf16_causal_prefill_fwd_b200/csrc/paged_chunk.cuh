@@ -183,7 +183,9 @@ struct ChStart {
 // By one warp of the block.
 __device__ __forceinline__ ChStart ch_start(const PagedAttn& p, int tpt) {
   const int lane = threadIdx.x & 31;
-  const Run run = plan_run(p, [&](const Request& x) { return ch_head_cost(p, x, tpt); });
+  const Run run = plan_run(
+      p, [&](const Request& x) { return ch_head_cost(p, x, tpt); },
+      [](const Request& x) { return x.nq > 0 ? (x.kv + kChN - 1) / kChN : 0; });
   ChStart d = {run.b, 0, 0, 0, run.count, run.first, run.per, run.req};
   if (run.count == 0) return d;
   const Request r = run.req;

@@ -201,13 +201,19 @@ struct Run {
 // requests whose rows overlap could make the line longer than the host's bound,
 // which is then refused -- and the request the run starts in by a scan over the
 // lanes. No other warp waits meanwhile.
-template <typename Cost>
-__device__ __forceinline__ Run plan_run(const PagedAttn& p, Cost cost) {
+//
+// No run is shorter than the root of a third of the longest unit (`longest` of each
+// request): a unit's parts are joined one after another, and a part costs the join
+// about a third of what a piece of work costs. One request of 4 tokens and 13k keys,
+// one head of 102 key blocks: 60 us in runs of one, 23 in runs of 5; over 64k keys
+// 72 us in runs of 4, 43 in runs of 12.
+template <typename Cost, typename Longest>
+__device__ __forceinline__ Run plan_run(const PagedAttn& p, Cost cost, Longest longest) {
   const int lane = threadIdx.x & 31;
   const bool report = blockIdx.x == 0;
   Request ahead = {0, 0, 0};
   if (lane < p.B) ahead = paged_request(p, lane, report);
-  int c = 0;
+  int c = 0, most = 0;
   long long sum = 0;
   Request x = {0, 0, 0};
 #pragma unroll 1
@@ -217,7 +223,9 @@ __device__ __forceinline__ Run plan_run(const PagedAttn& p, Cost cost) {
     if (b0 + 32 + lane < p.B) ahead = paged_request(p, b0 + 32 + lane, report);
     c = b0 + lane < p.B ? cost(x) : 0;
     sum += c;
+    if (b0 + lane < p.B) most = max(most, longest(x));
   }
+  most = __reduce_max_sync(0xffffffffu, most);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   Run r = {0, 0, 0, 0, 1, 1, {0, 0, 0}};
@@ -226,7 +234,8 @@ __device__ __forceinline__ Run plan_run(const PagedAttn& p, Cost cost) {
     return r;
   }
   const int total = static_cast<int>(sum) * p.Hkv;
-  r.per = (total + gridDim.x - 1) / static_cast<int>(gridDim.x);
+  r.per = max(static_cast<int>(sqrtf(most * (1.0f / 3.0f))),
+              static_cast<int>((total + gridDim.x - 1) / static_cast<int>(gridDim.x)));
   r.first = blockIdx.x * r.per;
   r.count = max(0, min(r.per, total - r.first));
   if (r.count == 0) return r;
