@@ -10,7 +10,10 @@ Lengths, tables and slots are int32 CUDA tensors read on the device only: no cal
 here copies from the device or waits for it, so each can be captured into a CUDA
 graph and replayed on new contents (a workspace or output given to a captured call
 has to live as long as the graph). Work goes to the current stream of the tensors'
-device, whichever device is current.
+device, whichever device is current, or to ``stream`` (a torch.cuda.Stream or a raw
+handle). What a call allocates then belongs to that stream, as under
+torch.cuda.stream(stream), and results are recorded on the caller's current stream as
+well; the inputs have to be ready there, and to live until the work is done.
 
 The checks and the marshalling are compiled (csrc/paged_binding.cpp): a decoding
 step makes these calls once per layer around kernels of a few microseconds.

@@ -9,11 +9,13 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty.h>
+#include <ATen/ops/record_stream.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
+#include <optional>
 #include <stdexcept>
 #include <string>
 
@@ -179,15 +181,37 @@ at::Tensor part(const at::Tensor& of, int64_t at, int64_t n) {
 }
 
 // The tensors' device as the current one for the call, and the stream to launch on.
+//
+// A stream the caller names is the current one while the call allocates: memory
+// belongs to the stream it was allocated on, so a workspace of the caller's current
+// stream could still be in use there when the kernels begin, and would be handed out
+// again when the call returns, under the kernels still running. What is returned is
+// recorded on the caller's stream too (result), where it may be read and let go.
 struct Launch {
   c10::cuda::OptionalCUDAGuard guard;
-  void* stream;
+  c10::cuda::OptionalCUDAStreamGuard on;
+  std::optional<c10::cuda::CUDAStream> callers;  // where the launch stream is another one
+  void* stream = nullptr;
   Launch(const c10::Device& dev, PyObject* s) {
     if (dev.is_cuda()) guard.set_device(dev);
-    if (given(s))
-      stream = reinterpret_cast<void*>(static_cast<uintptr_t>(PyLong_AsUnsignedLongLongMask(s)));
-    else
-      stream = dev.is_cuda() ? static_cast<void*>(c10::cuda::getCurrentCUDAStream(dev.index()).stream()) : nullptr;
+    uintptr_t handle = 0;
+    if (given(s)) {
+      handle = static_cast<uintptr_t>(PyLong_AsUnsignedLongLongMask(s));
+      stream = reinterpret_cast<void*>(handle);
+    }
+    if (!dev.is_cuda()) return;
+    const c10::cuda::CUDAStream now = c10::cuda::getCurrentCUDAStream(dev.index());
+    if (!given(s)) {
+      stream = now.stream();
+      return;
+    }
+    if (handle == 1) handle = 0;  // cudaStreamLegacy: the default stream
+    if (reinterpret_cast<cudaStream_t>(handle) == now.stream()) return;
+    callers = now;
+    on.reset_stream(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(handle), dev.index()));
+  }
+  void result(const at::Tensor& t) const {
+    if (callers && t.defined()) t.record_stream(*callers);
   }
 };
 
@@ -235,12 +259,13 @@ PyObject* slots(PyObject*, PyObject* const* a, Py_ssize_t n) {
     } else if (given(a[6]) || given(a[7])) {
       throw Refused("free_head goes with free_pages");
     }
+    Launch l(dev, a[8]);
     // one allocation: cu_seqlens, kv_lens, positions, slots, head
     const at::Tensor all = empty({2 * B + 2 + 2 * static_cast<int64_t>(total)}, at::kInt, dev);
     at::Tensor cu = part(all, 0, B + 1), kv = part(all, B + 1, B);
     at::Tensor pos = part(all, 2 * B + 1, total), slot = part(all, 2 * B + 1 + total, total);
     if (free && !head_out.defined()) head_out = part(all, 2 * B + 1 + 2 * static_cast<int64_t>(total), 1);
-    Launch l(dev, a[8]);
+    l.result(all);
     const int rc = fn_slots(table.ptr, table.row, table.width, static_cast<const int*>(ctx.data_ptr()),
                             static_cast<const int*>(nw.data_ptr()), int32(B, "batch"), total, ps, free, count, head,
                             free ? static_cast<int*>(head_out.data_ptr()) : nullptr, static_cast<int*>(cu.data_ptr()),
@@ -296,6 +321,7 @@ PyObject* fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
       scale = PyFloat_AsDouble(a[8]);
       if (scale == -1.0 && PyErr_Occurred()) return nullptr;
     }
+    Launch l(dev, a[14]);
     at::Tensor out, lse, ws;
     if (given(a[11])) {
       const at::Tensor* t = tensor(a[11]);
@@ -306,8 +332,10 @@ PyObject* fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
       out = *t;
     } else {
       out = empty({total, Hq, c.c.d_v}, at::kBFloat16, dev);
+      l.result(out);
     }
     if (want_lse) lse = empty({Hq, total}, at::kFloat, dev);
+    l.result(lse);
     if (given(a[13])) {
       const at::Tensor* t = tensor(a[13]);
       if (!t || t->device() != dev || !t->is_contiguous()) refuse("workspace", "contiguous on " + dev.str(), a[13]);
@@ -316,7 +344,6 @@ PyObject* fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (total > 0) {
       if (!ws.defined())
         ws = empty({static_cast<int64_t>(fn_ws(total, static_cast<int>(max_q), Hq, c.c.Hkv))}, at::kByte, dev);
-      Launch l(dev, a[14]);
       const int rc = fn_fwd(q.t->data_ptr(), q.stride, &c.c, table.ptr, table.row, table.width,
                             static_cast<const int*>(cu.data_ptr()), static_cast<const int*>(kv.data_ptr()),
                             int32(B, "batch"), total, static_cast<int>(max_q), Hq, causal, static_cast<float>(scale),

@@ -629,3 +629,70 @@ def test_calls_do_not_wait_for_the_stream():
     b2.attn_paged_fwd(*p.args())
     assert not busy.query()
     assert b2.check() == 0
+
+
+def owner(t):
+    """Handle of the stream whose pool t's memory is in."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("n,max_q", [(1, 1), (40, 40)])
+def test_calls_on_streams_given_by_name_share_no_memory(n, max_q, raw):
+    """stream= on two streams that are busy, with other inputs each, and memory taken and filled on the current stream
+    as soon as a call has returned: workspaces and results are each call's own."""
+    ps = [make([n] * 6, [900 + 31 * i for i in range(6)], 32, 8, 128, 16, seed=50 + i).cuda() for i in range(2)]
+    want = [b2.attn_paged_fwd(*p.args(), max_seqlen_q=max_q, return_lse=True) for p in ps]
+    size = b2.attn_paged_workspace_bytes(ps[0].q.shape[0], max_q, 32, 8)
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(2):
+        for s, p in zip(streams, ps):
+            with torch.cuda.stream(s):
+                torch.cuda._sleep(20_000_000)
+            got.append(b2.attn_paged_fwd(*p.args(), max_seqlen_q=max_q, return_lse=True, stream=s.cuda_stream if raw else s))
+            for like in (size, *(t.numel() * t.element_size() for t in got[-1])):
+                torch.full((like,), 0x7f, dtype=torch.uint8, device="cuda")
+    for s, (o, lse) in zip(streams * 2, got):
+        assert owner(o) == owner(lse) == s.cuda_stream
+    torch.cuda.synchronize()
+    assert b2.check() == 0
+    for (o, lse), (a, c) in zip(got, want * 2):
+        assert torch.equal(o, a) and torch.equal(lse, c)
+
+
+def test_slots_on_a_stream_given_by_name():
+    lens = ints([5, 0, 16]), ints([1, 3, 20])
+    table = torch.arange(12, dtype=torch.int32, device="cuda").view(3, 4)
+    free, head = ints(list(range(50, 70))), ints([1])
+    want = b2.paged_slots(table.clone(), *lens, 30, 16, free_pages=free, free_head=head)
+    side, tables = torch.cuda.Stream(), [table.clone() for _ in range(4)]
+    torch.cuda.synchronize()
+    got = []
+    for t in tables:
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(10_000_000)
+        got.append(b2.paged_slots(t, *lens, 30, 16, free_pages=free, free_head=head, stream=side))
+        torch.full((3 * 2 + 2 + 60,), 9, dtype=torch.int32, device="cuda")
+        assert all(owner(x) == side.cuda_stream for x in got[-1])
+    torch.cuda.synchronize()
+    assert b2.check() == 0
+    for r in got:
+        assert all(torch.equal(a, c) for a, c in zip(r, want))
+
+
+def test_the_default_stream_given_by_its_handle():
+    """0 and 1 both name it; under another current stream it is a stream of its own."""
+    p = make([1, 1], [100, 300], 8, 2, 128, 16, seed=52).cuda()
+    want = b2.attn_paged_fwd(*p.args(), max_seqlen_q=1)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        for handle in (0, 1):
+            o = b2.attn_paged_fwd(*p.args(), max_seqlen_q=1, stream=handle)
+            assert owner(o) == 0
+            torch.cuda.synchronize()
+            assert torch.equal(o, want)
+    assert b2.check() == 0
