@@ -94,10 +94,20 @@ struct ChCfg {
   static constexpr uint32_t FMT = FP8 ? 0u : 1u;
   static constexpr uint32_t IDESC_QK = idesc_dense(FMT, FMT, kChM, kChN, false);
   static constexpr uint32_t IDESC_PV = idesc_dense(FMT, FMT, kChM, DV, true);
-  // How far (log2) the running maximum may lag behind the true one before O is
-  // rescaled: probabilities reach 2^T, which fp16 holds up to 2^15.
-  static constexpr float T_LAG = FP8 ? 8.0f : 16.0f;
+  static constexpr float P_MAX = FP8 ? kHalfExp : 16.0f;  // probabilities reach 2^P_MAX
 };
+
+// Exponent that the largest probability of a row gets when its reference is moved;
+// it may then grow to P_MAX, by 16 (bf16), 8 or 2 binades, before O is rescaled. The
+// fp16 P of up to kChLongKeys keys lose at most n 2^-32 of a row's largest by rounding
+// (2^-12), those of more n 2^-38 (2^-8 at 2^30 keys). Room of 8, 4, 2 and 0 binades takes
+// 348, 353, 361 and 371 us for e4m3 chunks over 2-12k keys, of 16, 8, 4 and 0 1678, 1682,
+// 1704 and 1788 us for the long bf16 chunk; over many keys the maximum hardly moves.
+constexpr int kChLongKeys = 1 << 20;
+template <bool FP8>
+__device__ __forceinline__ float ch_p_exp(int kv) {
+  return !FP8 ? 0.0f : (kv <= kChLongKeys ? kHalfExp - 8.0f : kHalfExp - 2.0f);
+}
 
 // Key blocks of row tile `tile` of a request: 0 if the tile has no token; one
 // that masks everything for tokens that see no key.
@@ -322,7 +332,12 @@ __device__ __forceinline__ __half2 bits_half2(uint32_t x) {
   return h;
 }
 
-// Largest of three; NaN if one of them is.
+// Largest of two or three; NaN if one of them is.
+__device__ __forceinline__ float max2_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float r;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -810,7 +825,8 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
       end = w.end(t);
       }
 
-      float m_run = -INFINITY, l_run = 0.0f;
+      const float p_exp = ch_p_exp<FP8>(w.kv);
+      float m_ref = -INFINITY, l_run = 0.0f;  // probabilities are 2^(score - m_ref), at most 2^P_MAX
       const int kb = w.kb;
       for (int j = kb; j < end; ++j, ++g) {
         ok = __all_sync(0xffffffffu, paged_wait(bSFull + 8 * t, g & 1, abort_flag));
@@ -848,12 +864,13 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
         x0 = max3_nan(x0, __uint_as_float(sr[124]), __uint_as_float(sr[125]));
         x1 = max3_nan(x1, __uint_as_float(sr[126]), __uint_as_float(sr[127]));
         x0 = max3_nan(x0, x1, x2);
-        const float m_new = max3_nan(m_run, x0 * c_log2, x3 * c_log2);
-        const bool need = !(m_new <= m_run + C::T_LAG);  // true for NaN too
+        const float m_new = max2_nan(x0 * c_log2, x3 * c_log2);
+        const bool need = !(m_new <= m_ref + C::P_MAX);  // true for NaN too
         float alpha = 1.0f;
         if (need) {
-          alpha = ex2_approx(m_run - m_new);
-          m_run = m_new;
+          const float to = m_new - p_exp;
+          alpha = ex2_approx(m_ref - to);
+          m_ref = to;
         }
         l_run *= alpha;
 
@@ -861,7 +878,7 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
         // All on the MUFU unit: what these warps lack is issue slots (and, under the power cap, energy), and a
         // polynomial for one score in four on the FMA pipe took long chunks 1765 us for 1690, e4m3 chunks 403 for
         // 362; for one in eight 1727 and 393.
-        const float nm = m_run == -INFINITY ? 0.0f : -m_run;
+        const float nm = m_ref == -INFINITY ? 0.0f : -m_ref;
         float sa = 0.f, sb = 0.f, sc = 0.f, sd = 0.f;
 #pragma unroll
         for (int c = 0; c < 128; c += 4) {
@@ -911,8 +928,8 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
       const bool whole = w.whole != 0;
       const int64_t part =
           static_cast<int64_t>(2 * blockIdx.x + (w.kb > 0 ? 0 : 1)) * p.slot_rows + t * tpt * p.G + r;
-      const float v_mult = FP8 ? __ldg(p.v_scale + w.h) : 1.0f;
-      const float inv = !whole ? 1.0f : (l_run == 0.0f ? 0.0f : v_mult / l_run);
+      const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
+      const float v_mult = !FP8 ? 1.0f : (l_run == 0.0f ? 0.0f : __ldg(p.v_scale + w.h));
       const int hq = w.h * p.G + rhead;
       __nv_bfloat16* orow = p.o + (static_cast<int64_t>(w.t0 + (real ? tok : 0)) * p.Hq + (real ? hq : 0)) * DV;
       // parts: [slot][DV / 4][row][4], whole lines for a warp's 32 rows
@@ -927,7 +944,7 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
           uint32_t y[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            y[i] = pack_bf16x2(__uint_as_float(orr[2 * i]) * inv, __uint_as_float(orr[2 * i + 1]) * inv);
+            y[i] = pack_bf16x2(__uint_as_float(orr[2 * i]) * inv * v_mult, __uint_as_float(orr[2 * i + 1]) * inv * v_mult);
           st_global_32b(orow + cc, y);
           st_global_32b(orow + cc + 16, y + 8);
         } else if (real) {
@@ -938,11 +955,11 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
         }
       }
       if (real && !whole) {
-        p.part_ml[2 * part] = m_run;
+        p.part_ml[2 * part] = m_ref;
         p.part_ml[2 * part + 1] = l_run;
       } else if (real && p.lse != nullptr) {
         p.lse[static_cast<int64_t>(hq) * p.T + w.t0 + tok] =
-            l_run == 0.0f ? -INFINITY : (m_run + fast_log2(l_run)) * kLn2;
+            l_run == 0.0f ? -INFINITY : (m_ref + fast_log2(l_run)) * kLn2;
       }
       tc_fence_before();
       mbar_arrive(bOEmpty + 8 * t);

@@ -18,6 +18,12 @@ constexpr int kPagedInvalid = -1;                      // B200ATTN_ERR_INVALID
 constexpr int kPagedNoPages = -6;                      // B200ATTN_ERR_PAGES
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// Probabilities in fp16 (e4m3 caches) are held as 2^x times their value, so that the
+// largest of a row is near 2^15 and uses the type's range: rounding takes at most
+// 2^-25 off any of them, so that a row of n keys, its small probabilities under the
+// smallest subnormal among them, loses at most n 2^-40 of its largest. The factor is
+// in the row sum, too; the m that is kept with it is less by x.
+constexpr float kHalfExp = 15.0f;
 
 // Status word of these kernels; b200attn_check reads it with the other one.
 __device__ int g_paged_status;

@@ -416,7 +416,8 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<DQK, DV, FP8, NT>::BLOCKS)
             alpha[j][i] = mn > m[j][i] ? ex2_approx(m[j][i] - mn) : 1.0f;
             moved |= mn > m[j][i];
             m[j][i] = mn;
-            const float ref = mn == -INFINITY ? 0.0f : mn;  // nothing seen yet: every probability is 0
+            // nothing seen yet: every probability is 0
+            const float ref = (mn == -INFINITY ? 0.0f : mn) - (FP8 ? kHalfExp : 0.0f);
             float sum = 0.0f;
 #pragma unroll
             for (int gi = 0; gi < C::KG; ++gi) {
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<DQK, DV, FP8, NT>::BLOCKS)
         if (lane < 4) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            s_ml[(warp * 8 + 2 * lane + i) * 2] = m[j][i];
+            s_ml[(warp * 8 + 2 * lane + i) * 2] = m[j][i] - (FP8 ? kHalfExp : 0.0f);
             s_ml[(warp * 8 + 2 * lane + i) * 2 + 1] = l[j][i];
           }
         }
@@ -525,8 +526,8 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<DQK, DV, FP8, NT>::BLOCKS)
           }
           if (whole) {
             const int tok = r / p.G, hq = w.h * p.G + r - tok * p.G;
-            const float inv = ll == 0.0f ? 0.0f : (FP8 ? __ldg(p.v_scale + w.h) : 1.0f) / ll;
-            p.o[(static_cast<int64_t>(w.r.t0 + tok) * p.Hq + hq) * DV + td] = __float2bfloat16(acc * inv);
+            const float x = ll == 0.0f ? 0.0f : acc * (1.0f / ll) * (FP8 ? __ldg(p.v_scale + w.h) : 1.0f);
+            p.o[(static_cast<int64_t>(w.r.t0 + tok) * p.Hq + hq) * DV + td] = __float2bfloat16(x);
             if (p.lse != nullptr && td == 0)
               p.lse[static_cast<int64_t>(hq) * p.T + w.r.t0 + tok] =
                   ll == 0.0f ? -INFINITY : (mm + fast_log2(ll)) * kLn2;

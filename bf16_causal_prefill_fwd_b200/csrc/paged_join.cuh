@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(128) paged_join_few_kernel(const PagedAttn p) 
     int tok, hq;
     join_place(p, e, r, tok, hq);
     p.o[(static_cast<int64_t>(tok) * p.Hq + hq) * DV + td] =
-        __float2bfloat16(all.l == 0.0f ? 0.0f : sum * (v_scale / all.l));
+        __float2bfloat16(all.l == 0.0f ? 0.0f : sum * (1.0f / all.l) * v_scale);
     if (p.lse != nullptr && td == 0) p.lse[static_cast<int64_t>(hq) * p.T + tok] = all.lse();
     __syncthreads();  // s_o is written again
   }
@@ -137,11 +137,12 @@ __global__ void __launch_bounds__(128) paged_join_rows_kernel(const PagedAttn p)
 #pragma unroll
       for (int n = 0; n < 4; ++n) join_add(acc[n], o[n], keep, take);
     }
-    const float inv = j.l == 0.0f ? 0.0f : v_scale / j.l;
+    const float inv = j.l == 0.0f ? 0.0f : 1.0f / j.l, vs = j.l == 0.0f ? 0.0f : v_scale;
 #pragma unroll
     for (int n = 0; n < 4; ++n)
       *reinterpret_cast<uint2*>(&s_o[lr][2 * (l8 + 8 * n)]) =
-          make_uint2(pack_bf16x2(acc[n].x * inv, acc[n].y * inv), pack_bf16x2(acc[n].z * inv, acc[n].w * inv));
+          make_uint2(pack_bf16x2(acc[n].x * inv * vs, acc[n].y * inv * vs),
+                     pack_bf16x2(acc[n].z * inv * vs, acc[n].w * inv * vs));
     int tok, hq;
     if (p.lse != nullptr && l8 == 0 && r0 + lr < e.nrows) {
       join_place(p, e, r, tok, hq);

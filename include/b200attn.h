@@ -453,7 +453,9 @@ size_t b200attn_paged_fwd_workspace_bytes(int total, int max_seqlen_q, int Hq, i
  * cache  bf16: products in bf16, fp32 accumulation. e4m3: codes are taken
  *        exactly, Q after a power of two per row as fp16 or as the sum of two e4m3
  *        numbers (what is 2^-10 of the row's largest element or more keeps all its
- *        bits), the probabilities as fp16; fp32 accumulation, per-head scales.
+ *        bits), the probabilities as fp16 times a power of two (rounding takes no
+ *        more than n 2^-32 of a row's largest from n <= 2^20 keys, n 2^-38 from
+ *        more); fp32 accumulation, per-head scales.
  * block_table  int32 [batch, table_width], rows table_stride apart. Only the
  *        entries of the first kv_lens[b] rows are read. An entry that is no page
  *        reads as zero keys and values, and INVALID is reported.

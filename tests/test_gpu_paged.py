@@ -494,6 +494,100 @@ def test_offsets_past_32_bits():
     del kc, vc
 
 
+# ------------------------------------------------------------------------------------------- many keys
+
+def repeated(q, k, v, row, kv, scale):
+    """64-bit attention of q [n, d] without a mask over kv keys: the pages `row` of k and v [pages, page_size, d], which
+    it may name many times. Returns o, lse and sum_j p_j |v_j| / l."""
+    ps = k.shape[1]
+    full, rest = kv // ps, kv % ps
+    times = torch.bincount(row[:full].long(), minlength=k.shape[0])[:, None].expand(-1, ps).clone()
+    if rest:
+        times[int(row[full]), :rest] += 1
+    x = q.double() @ k.flatten(0, 1).double().T * scale
+    x[:, times.flatten() == 0] = -math.inf
+    m = x.amax(1, keepdim=True)
+    w = torch.exp(x - m) * times.flatten()
+    l = w.sum(1, keepdim=True)
+    vv = v.flatten(0, 1).double()
+    return w @ vv / l, (m + l.log())[:, 0], w @ vv.abs() / l
+
+
+def lost(n_new, G, kv):
+    """What the fp16 probabilities of one part of a row may miss of its largest: 2^-25 each, the largest held at 2^15 by
+    the decoding kernel, at 2^7 or more by the other, at 2^13 or more above 2^20 keys."""
+    return kv * 2.0 ** -(40 if n_new * G <= 16 else (32 if kv <= 1 << 20 else 38))
+
+
+@pytest.mark.parametrize("n_new,kv,d", [(1, (1 << 18) + 37, 128), (1, (1 << 18) + 37, 192), (8, (1 << 18) + 37, 128),
+                                        (8, (1 << 18) + 37, 192), (8, (1 << 20) + 5, 128)])
+def test_small_probabilities_of_a_long_e4m3_context_count(n_new, kv, d):
+    """A first key 26 binades above all others, which together hold 2^-8 or more of the weight, in units that no block
+    shares with another: the columns of V that only they have."""
+    G, ps = 4, 64
+    B = torch.cuda.get_device_properties(0).multi_processor_count * (3 if n_new == 1 else 1)
+    k, v = torch.zeros(2, ps, d), torch.zeros(2, ps, 128)
+    k[..., 0], v[..., 1::2] = -0.1875, 1.0
+    k[0, 0, 0], v[0, 0] = 18.0, 0.0
+    v[0, 0, ::2] = 1.0
+    q = torch.randn(n_new, d, generator=torch.Generator().manual_seed(61)).to(torch.bfloat16)
+    q[:, 0] = 1.0
+    row = torch.ones(kv // ps + 1, dtype=torch.int32)
+    row[0] = 0
+    o, lse, _ = repeated(q, k, v, row, kv, 1.0)
+    one = torch.ones(1, device="cuda")
+    got, got_lse = b2.attn_paged_fwd(
+        q.cuda()[:, None].expand(-1, G, -1).repeat(B, 1, 1), *(x.to(torch.float8_e4m3fn).cuda()[:, :, None] for x in (k, v)),
+        row.cuda().repeat(B, 1), ints([n_new * i for i in range(B + 1)]), ints([kv] * B), max_seqlen_q=n_new, causal=False,
+        softmax_scale=1.0, k_scale=one, v_scale=one, return_lse=True)
+    assert b2.check() == 0
+    # beside what fp16 loses: a half step of fp16 and of bf16, scores (2^-24 of 18 or less) and the exponential, and
+    # kv / 16 fp32 accumulations that may cut off
+    off = 2.0 ** -11 + 2.0 ** -8 + 18 * 2.0 ** -23 + 2.0 ** -22 + kv / 16 * 2.0 ** -23
+    bound = (o.abs() * off + lost(n_new, G, kv))[None, :, None]
+    assert bool((bound[..., 1::2] < o[None, :, None, 1::2] / 4).all())
+    assert bool(((got.view(B, n_new, G, 128).double().cpu() - o[None, :, None]).abs() <= bound).all())
+    assert bool(((got_lse.view(G, B, n_new).double().cpu() - lse).abs() <= 2.0 ** -18 + kv / 64 * 2.0 ** -24).all())
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n_new,kv", [(1, (1 << 20) - 9), (1, (1 << 21) + 3), (9, (1 << 20) - 9), (9, (1 << 20) + 1),
+                                      (40, (1 << 21) + 3)])
+def test_long_contexts_with_a_rising_maximum(n_new, kv, e4m3):
+    """Pages named many times, in the order of the first row's largest score, so that its maximum moves by small steps
+    over the whole context."""
+    H, G, d, ps = 2, 2, 128, 64
+    g = torch.Generator().manual_seed(kv % 1000 + n_new)
+    q = torch.randn(n_new, H * G, d, generator=g).to(torch.bfloat16)
+    k, v = (torch.randn(300, ps, H, d, generator=g) * s for s in (2.0, 1.0))
+    kw = {}
+    if e4m3:
+        kw = dict(k_scale=torch.full((H,), 0.02), v_scale=torch.full((H,), 0.011))
+        kc, vc = ((x / s[0]).clamp(-448.0, 448.0).to(torch.float8_e4m3fn) for x, s in zip((k, v), kw.values()))
+        k, v = (c.float() * s[0] for c, s in zip((kc, vc), kw.values()))
+    else:
+        kc, vc = k.to(torch.bfloat16), v.to(torch.bfloat16)
+        k, v = kc, vc
+    peak = (k[:, :, 0].double() @ q[0, 0].double()).amax(1)
+    order = torch.argsort(peak).to(torch.int32)
+    pages = kv // ps + 1
+    row = order[torch.arange(pages) * 300 // pages]
+    got, got_lse = b2.attn_paged_fwd(q.cuda(), kc.cuda(), vc.cuda(), row.cuda()[None], ints([0, n_new]), ints([kv]),
+                                     max_seqlen_q=n_new, causal=False, return_lse=True,
+                                     **{n: x.cuda() for n, x in kw.items()})
+    assert b2.check() == 0
+    half = 2.0 ** -11 if e4m3 else 2.0 ** -8
+    for h in range(H * G):
+        hk = h // G
+        o, lse, a = repeated(q[:, h], k[:, :, hk], v[:, :, hk], row, kv, d ** -0.5)
+        reach = (q[:, h].double().abs() @ k[:, :, hk].flatten(0, 1).double().abs().T).amax(1) * d ** -0.5
+        score = ((d + 2) * 2.0 ** -24 * reach + 2.0 ** -22)[:, None]
+        bound = a * (half + 2 * score + kv / 16 * 2.0 ** -23) + o.abs() * 2.0 ** -8 + a.amax(1, keepdim=True).clamp(min=1.0) * (
+            lost(n_new, G, kv) if e4m3 else 0.0)
+        assert bool(((got[:, h].double().cpu() - o).abs() <= bound).all()), h
+        assert bool(((got_lse[h].double().cpu() - lse).abs() <= score[:, 0] + 2.0 ** -22 * (2 + lse.abs()) + kv / 64 * 2.0 ** -24).all())
+
+
 # ------------------------------------------------------------------------------------------- as a server uses them
 
 def dense(q, k, v, n_ctx):
