@@ -816,11 +816,12 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
         mbar_arrive(bQFull + 8 * t);
       }
       ++units;
-      c_log2 = fmaxf(c_log2, 1e-30f);  // a zero scale behaves as a tiny one
       // keys this row sees: j <= see; the tile's first row sees fewest
       const int off = p.causal ? w.kv - w.nq : w.kv - 1;
       see = p.causal ? min(off + tok, w.kv - 1) : off;
       see_all = p.causal ? min(off + w.tok0 + t * tpt, w.kv - 1) : off;
+      // a zero scale behaves as a tiny one; a NaN stays, but for a row that sees no key
+      if (c_log2 < 1e-30f || see < 0) c_log2 = 1e-30f;
 
       end = w.end(t);
       }

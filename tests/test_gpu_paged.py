@@ -441,6 +441,24 @@ def test_nan_reaches_the_rows_that_see_it_and_no_other(n, max_q, e4m3):
             assert bool(lse.T.isnan().cpu()[hit].all())
 
 
+@pytest.mark.parametrize("which", ["k_scale", "v_scale"])
+@pytest.mark.parametrize("q_lens,kv_lens,max_q", [([2, 2, 2], [90, 1, 0], 2), ([40, 40, 3], [200, 7, 0], 40)])
+def test_nan_scale_gives_nan_in_its_heads_rows_that_see_a_key(q_lens, kv_lens, max_q, which):
+    p = make(q_lens, kv_lens, 8, 2, 128, 16, True, seed=26)
+    ref = run(p, max_seqlen_q=max_q)
+    getattr(p, which)[1] = math.nan
+    o, lse = run(p, max_seqlen_q=max_q)
+    hit = ref[1] > -math.inf
+    hit[:4] = False
+    assert bool(hit.any()) and bool((ref[1][4:] == -math.inf).any())
+    assert bool(o.transpose(0, 1)[hit].isnan().all()) and torch.equal(o.transpose(0, 1)[~hit], ref[0].transpose(0, 1)[~hit])
+    assert torch.equal(lse[~hit], ref[1][~hit])
+    if which == "k_scale":
+        assert bool(lse[hit].isnan().all())
+    else:
+        assert torch.equal(lse, ref[1])
+
+
 @pytest.mark.parametrize("n,max_q", [(1, 1), (40, 40)])
 def test_infinite_query_gives_nan_in_its_row_only(n, max_q):
     for e4m3 in (False, True):
