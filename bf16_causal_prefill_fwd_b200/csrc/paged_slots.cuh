@@ -17,8 +17,8 @@
 // step of 13 requests takes 5.1 us a call in a loop, 512 requests with 16 thousand
 // new tokens 7.5 us; of either the launch is about 3.
 //
-// Anything that does not fit (a negative length, more tokens than `total`, more
-// pages than a table row holds or than are free) is found before any table
+// Anything that does not fit (a negative length, one past 32 bits, more tokens than
+// `total`, more pages than a table row holds or than are free) is found before any table
 // entry or the head is written: the step is then empty (cu and kv zero, every
 // slot -1) and the status word says why.
 #pragma once
@@ -61,6 +61,11 @@ __device__ __forceinline__ int last_not_above(const int* s, int n, int x) {
   return lo;
 }
 
+// Pages of c rows; c + ps may pass 2^31.
+__device__ __forceinline__ int pages_of(int c, int ps) {
+  return static_cast<int>((static_cast<uint32_t>(c) + ps - 1) / static_cast<uint32_t>(ps));
+}
+
 __global__ void __launch_bounds__(kSlotsThreads) paged_slots_kernel(const PagedSlots p) {
   extern __shared__ int sm[];
   int* s_cu = sm;               // [B + 1]
@@ -88,12 +93,12 @@ __global__ void __launch_bounds__(kSlotsThreads) paged_slots_kernel(const PagedS
       const int c = __ldg(p.ctx + b);
       s_ctx[b] = c;
       n = __ldg(p.nw + b);
-      const int64_t want = (static_cast<int64_t>(c) + n + ps - 1) / ps;
-      if (c < 0 || n < 0 || n > p.total || want > p.width) {
+      const int64_t rows = static_cast<int64_t>(c) + n, want = (rows + ps - 1) / ps;
+      if (c < 0 || n < 0 || n > p.total || want > p.width || rows > 0x7fffffff) {
         bad = -kPagedInvalid;
         n = 0;
       } else if (alloc) {
-        fresh = static_cast<int>(want) - (c + ps - 1) / ps;
+        fresh = static_cast<int>(want) - pages_of(c, ps);
       }
     }
     // n <= total < 2^30 and at most kSlotsThreads of them: saturate so that no sum overflows
@@ -142,7 +147,7 @@ __global__ void __launch_bounds__(kSlotsThreads) paged_slots_kernel(const PagedS
   if (alloc && !bad) {
     for (int j = at; j < run.y; j += step) {
       const int b = last_not_above(s_fr, p.B, j);
-      const int held = (s_ctx[b] + ps - 1) / ps;
+      const int held = pages_of(s_ctx[b], ps);
       p.table[b * p.table_stride + held + (j - s_fr[b])] = __ldg(p.free_pages + head + j);
     }
   }
@@ -154,7 +159,7 @@ __global__ void __launch_bounds__(kSlotsThreads) paged_slots_kernel(const PagedS
       const int b = last_not_above(s_cu, p.B, t);
       const int c = s_ctx[b];
       pos = c + t - s_cu[b];
-      const int idx = pos / ps, held = (c + ps - 1) / ps;
+      const int idx = pos / ps, held = pages_of(c, ps);
       const int page = alloc && idx >= held ? __ldg(p.free_pages + head + s_fr[b] + idx - held)
                                             : p.table[b * p.table_stride + idx];
       const int64_t at_slot = static_cast<int64_t>(page) * ps + (pos - idx * ps);

@@ -386,6 +386,7 @@ typedef struct {
  *        the entries the new tokens need are written, others never are.
  * context_lens, new_lens  int32 [batch]: tokens cached / new in this step (each
  *        may be 0); context_lens[b] + new_lens[b] <= table_width * page_size
+ *        and < 2^31
  * total  rows of positions and slots; the new tokens may be fewer (a padded
  *        step): the rows behind them get position 0 and slot -1
  * page_size  any size >= 1
@@ -401,7 +402,7 @@ typedef struct {
  * batch <= 16384, total < 2^30.
  *
  * A step that does not fit (negative lengths, more than `total` new tokens, a
- * request longer than its table row: INVALID; fewer free pages than needed:
+ * request longer than its table row or of 2^31 tokens or more: INVALID; fewer free pages than needed:
  * PAGES) is reported by b200attn_check and gives an empty step: cu_seqlens and
  * kv_lens 0, every slot -1, the table unchanged, *free_head_out = *free_head.
  * A negative table entry among those read gives its tokens slot -1 and INVALID.

@@ -240,6 +240,34 @@ def test_slots_that_do_not_fit_give_an_empty_step(bad):
     assert b2.check() == 0
 
 
+@pytest.mark.parametrize("ps", [1 << 20, (1 << 31) - 1])
+def test_slots_of_lengths_near_32_bits(ps):
+    """The last position that 32 bits hold, with a page taken for it, is given; one token more does not fit."""
+    last = 2 ** 31 - 1
+    held, free, head = -(-(last - 5) // ps), [9, 9, 0, 9, 9], 2
+    width = max(2, held + 1)
+    for ctx, new, fits in ((last - 5, 5, True), (last, 0, True), (last - 5, 6, False), (last, 1, False)):
+        table = torch.full((2, width), -1, dtype=torch.int32)
+        table[0] = torch.arange(width)
+        before = table.cuda()
+        t = before.clone()
+        got = b2.paged_slots(t, ints([ctx, 0]), ints([new, 1]), 9, ps, free_pages=ints(free), free_head=ints([head]))
+        assert b2.check() == (0 if fits else -1)
+        if fits:
+            want = before.clone()
+            want[1, 0] = free[head]
+            page = (last - 1) // ps
+            slot = page * ps + (last - 1) % ps
+            assert got[0].tolist() == [0, new, new + 1] and got[1].tolist() == [ctx + new, 1]
+            assert got[2].tolist() == list(range(ctx, ctx + new)) + [0] * (9 - new)
+            assert got[3].tolist()[:new] == [slot - new + 1 + i for i in range(new)] and got[4].tolist() == [head + 1]
+            assert got[3].tolist()[new:] == [0] + [-1] * (8 - new)
+        else:
+            want = before
+            assert got[0].tolist() == [0, 0, 0] and got[3].tolist() == [-1] * 9 and got[4].tolist() == [head]
+        assert torch.equal(t, want)
+
+
 def test_slots_of_an_unset_table_entry_are_reported():
     got = b2.paged_slots(ints([[4, -1]]), ints([14]), ints([4]), 4, 16)
     assert b2.check() == -1
