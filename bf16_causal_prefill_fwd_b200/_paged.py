@@ -86,6 +86,7 @@ def paged_append_kv(k, v, k_cache, v_cache, slots, *, k_scale=None, v_scale=None
 
 
 def attn_paged_workspace_bytes(total: int, max_seqlen_q: int, Hq: int, Hkv: int) -> int:
+    """Bytes of a workspace for attn_paged_fwd with `total` rows of q; enough for fewer rows and tokens as well."""
     return int(_b.load_library().b200attn_paged_fwd_workspace_bytes(total, max_seqlen_q, Hq, Hkv))
 
 

@@ -370,8 +370,11 @@ int b200attn_paged_append(const void* k, const void* v, size_t k_stride, size_t 
 
 size_t b200attn_paged_fwd_workspace_bytes(int total, int max_seqlen_q, int Hq, int Hkv) {
   if (total < 1 || max_seqlen_q < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return 0;
-  if (few_rows(max_seqlen_q, Hq / Hkv)) return parts_of(b200p::kDecMaxBlocks, b200p::kDecMaxRows).bytes;
-  return parts_of(b200p::kChMaxBlocks, chunk_rows(total, Hq / Hkv)).bytes;
+  // never less than for fewer tokens, whichever kernel takes those
+  const size_t few = parts_of(b200p::kDecMaxBlocks, b200p::kDecMaxRows).bytes;
+  if (few_rows(max_seqlen_q < total ? max_seqlen_q : total, Hq / Hkv)) return few;
+  const size_t many = parts_of(b200p::kChMaxBlocks, chunk_rows(total, Hq / Hkv)).bytes;
+  return many > few ? many : few;
 }
 
 int b200attn_paged_fwd(const void* q, size_t q_stride, const b200attn_paged_cache* cache, const int* block_table,
@@ -384,6 +387,7 @@ int b200attn_paged_fwd(const void* q, size_t q_stride, const b200attn_paged_cach
     return B200ATTN_ERR_INVALID;
   if (Hq % cache->Hkv != 0 || (causal != 0 && causal != 1) || !std::isfinite(softmax_scale)) return B200ATTN_ERR_INVALID;
   if (total == 0) return B200ATTN_OK;  // no new tokens
+  if (max_seqlen_q > total) max_seqlen_q = total;
   if (!q || !o || !block_table || !cu_seqlens || !kv_lens) return B200ATTN_ERR_INVALID;
   if (!aligned(q, 16) || !aligned(o, 32) || !aligned(block_table, 4) || !aligned(cu_seqlens, 4) ||
       !aligned(kv_lens, 4) || !aligned(lse, 4) || !rows_ok(q_stride, total, Hq, cache->d_qk))
@@ -397,7 +401,7 @@ int b200attn_paged_fwd(const void* q, size_t q_stride, const b200attn_paged_cach
       static_cast<int64_t>(batch) * cache->Hkv * (keys / 64 /* the smallest tile */ + 1) >= (int64_t(1) << 31))
     return B200ATTN_ERR_UNSUPPORTED;
   if (!few_rows(max_seqlen_q, G)) {  // so is the line of key blocks of all pairs of row tiles
-    const int64_t per = 2 * (b200p::kChM / G), most = max_seqlen_q < total ? max_seqlen_q : total;
+    const int64_t per = 2 * (b200p::kChM / G), most = max_seqlen_q;
     const int64_t each = batch * ((most + per - 1) / per), packed = total / per + batch;
     if ((each < packed ? each : packed) * cache->Hkv * (keys / b200p::kChN + 1 + b200p::kChUnitCost) >= (int64_t(1) << 31))
       return B200ATTN_ERR_UNSUPPORTED;

@@ -434,7 +434,8 @@ int b200attn_paged_append(const void* k, const void* v, size_t k_stride, size_t 
 
 /*
  * b200attn_paged_fwd_workspace_bytes -- device workspace b200attn_paged_fwd
- * needs, from sizes alone. Returns 0 for invalid sizes.
+ * needs, from sizes alone: never less for more tokens, so that what is enough for a
+ * server's largest step is for its smaller ones. Returns 0 for invalid sizes.
  */
 size_t b200attn_paged_fwd_workspace_bytes(int total, int max_seqlen_q, int Hq, int Hkv);
 
@@ -467,7 +468,8 @@ size_t b200attn_paged_fwd_workspace_bytes(int total, int max_seqlen_q, int Hq, i
  *        table_width * page_size < 2^30
  * total  rows of q and o
  * max_seqlen_q  upper bound on the new tokens of any request, known on the host
- *        (`total` if nothing better is); a request with more is skipped and
+ *        (`total` if nothing better is, and what a larger one is taken as); a
+ *        request with more is skipped and
  *        INVALID reported, like one whose cu_seqlens or kv_lens do not fit
  * o      bf16 [total, Hq, d_v], contiguous, 32-byte aligned
  * lse    optional fp32 [Hq, total]

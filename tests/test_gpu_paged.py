@@ -836,3 +836,13 @@ def test_the_default_stream_given_by_its_handle():
             torch.cuda.synchronize()
             assert torch.equal(o, want)
     assert b2.check() == 0
+
+
+@pytest.mark.parametrize("n,max_q", [(1, 8), (5, 8), (2, 100)])
+def test_a_workspace_of_the_stated_size_serves_the_call_and_smaller_ones(n, max_q):
+    p = make([n], [300], 32, 8, 128, 16, seed=71)
+    size = b2.attn_paged_workspace_bytes(n, max_q, 32, 8)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    check_attention(p, *run(p, max_seqlen_q=max_q, workspace=ws))
+    p = make([1], [300], 32, 8, 128, 16, seed=72)
+    check_attention(p, *run(p, max_seqlen_q=1, workspace=ws))

@@ -248,3 +248,26 @@ def test_workspace_sizes(real):
     assert 0 < few < 16 << 20 and ws(64, 4, 32, 8) == few             # 16 rows per key/value head
     assert ws(64, 5, 32, 8) > few                                     # the many-rows kernel: 256 rows a slot
     assert ws(5, 5, 32, 8) < ws(64, 64, 32, 8) == ws(5000, 5000, 32, 8) < 64 << 20
+
+
+def test_a_workspace_for_more_tokens_is_enough_for_fewer(real):
+    """As large as the call itself needs with the same arguments, and growing with both."""
+    ws = real.b200attn_paged_fwd_workspace_bytes
+    sizes = [1, 2, 3, 4, 5, 6, 7, 8, 11, 12, 16, 17, 31, 64, 65, 1000]
+    for hq, hkv in ((32, 8), (8, 2), (16, 16), (28, 4), (128, 1), (5, 1)):
+        for total in sizes:
+            for max_q in sizes:
+                assert ws(total, max_q, hq, hkv) == ws(total, min(max_q, total), hq, hkv)
+                assert all(ws(t, m, hq, hkv) <= ws(total, max_q, hq, hkv) for t in sizes if t <= total
+                           for m in sizes if m <= max_q)
+
+
+@pytest.mark.parametrize("total,max_q,hq", [(1, 8, 32), (3, 64, 8), (4, 5, 32), (5, 5, 32), (64, 2, 32)])
+def test_the_stated_workspace_is_enough_for_the_call(real, total, max_q, hq):
+    hkv = hq // 4
+    need = real.b200attn_paged_fwd_workspace_bytes(total, max_q, hq, hkv)
+    args = dict(stride=hq * D, total=total, maxq=max_q, hq=hq)
+    c = cache(h=hkv, token=hkv * D, page=PS * hkv * D)
+    assert c_attn(real, c, wsb=need - 1, **args) == -5
+    if not torch.cuda.is_available():  # past the checks: no device
+        assert c_attn(real, c, wsb=need, **args) == -3
