@@ -394,17 +394,19 @@ int b200attn_paged_fwd(const void* q, size_t q_stride, const b200attn_paged_cach
     return B200ATTN_ERR_INVALID;
   const int G = Hq / cache->Hkv;
   if (G > 128) return B200ATTN_ERR_UNSUPPORTED;
-  // the kernels count query rows and key tiles in 32 bits
+  // the kernels count query rows and the line of key tiles in 32 bits
+  constexpr int64_t limit = int64_t(1) << 31;
   const int64_t keys = static_cast<int64_t>(table_width) * cache->page_size;
-  if (keys >= (int64_t(1) << 30) || table_stride > 0x7fffffff ||
-      static_cast<int64_t>(total) * Hq >= (int64_t(1) << 31) ||
-      static_cast<int64_t>(batch) * cache->Hkv * (keys / 64 /* the smallest tile */ + 1) >= (int64_t(1) << 31))
+  const int64_t lines = static_cast<int64_t>(batch) * cache->Hkv;
+  if (keys >= limit / 2 || table_stride > 0x7fffffff || static_cast<int64_t>(total) * Hq >= limit || lines >= limit)
     return B200ATTN_ERR_UNSUPPORTED;
-  if (!few_rows(max_seqlen_q, G)) {  // so is the line of key blocks of all pairs of row tiles
+  if (few_rows(max_seqlen_q, G)) {
+    if (lines * (keys / 64 /* the smallest tile */ + 1) >= limit) return B200ATTN_ERR_UNSUPPORTED;
+  } else {  // pairs of row tiles, by the bound on new tokens or by the rows there are
     const int64_t per = 2 * (b200p::kChM / G), most = max_seqlen_q;
     const int64_t each = batch * ((most + per - 1) / per), packed = total / per + batch;
-    if ((each < packed ? each : packed) * cache->Hkv * (keys / b200p::kChN + 1 + b200p::kChUnitCost) >= (int64_t(1) << 31))
-      return B200ATTN_ERR_UNSUPPORTED;
+    const int64_t units = (each < packed ? each : packed) * cache->Hkv;
+    if (units >= limit || units * (keys / b200p::kChN + 1 + b200p::kChUnitCost) >= limit) return B200ATTN_ERR_UNSUPPORTED;
   }
   const size_t need = b200attn_paged_fwd_workspace_bytes(total, max_seqlen_q, Hq, cache->Hkv);
   if (!workspace || workspace_bytes < need || !aligned(workspace, 16)) return B200ATTN_ERR_WORKSPACE;
@@ -452,10 +454,6 @@ int b200attn_paged_fwd(const void* q, size_t q_stride, const b200attn_paged_cach
       return fp8 ? launch_few<128, true>(cache, p, sm_count, device, st) : launch_few<128, false>(cache, p, sm_count, device, st);
     return fp8 ? launch_few<192, true>(cache, p, sm_count, device, st) : launch_few<192, false>(cache, p, sm_count, device, st);
   }
-  // key blocks of all units, counted in 32 bits
-  const int64_t pairs = static_cast<int64_t>(total) / (2 * (b200p::kChM / G)) + batch;
-  if (pairs * cache->Hkv >= (int64_t(1) << 31) || pairs * cache->Hkv * (keys / b200p::kChN + 1 + b200p::kChUnitCost) >= (int64_t(1) << 31))
-    return B200ATTN_ERR_UNSUPPORTED;
   if (cache->d_qk == 128)
     return fp8 ? launch_chunk<128, true>(cache, p, sm_count, device, st) : launch_chunk<128, false>(cache, p, sm_count, device, st);
   return fp8 ? launch_chunk<192, true>(cache, p, sm_count, device, st) : launch_chunk<192, false>(cache, p, sm_count, device, st);

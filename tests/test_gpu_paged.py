@@ -846,3 +846,17 @@ def test_a_workspace_of_the_stated_size_serves_the_call_and_smaller_ones(n, max_
     check_attention(p, *run(p, max_seqlen_q=max_q, workspace=ws))
     p = make([1], [300], 32, 8, 128, 16, seed=72)
     check_attention(p, *run(p, max_seqlen_q=1, workspace=ws))
+
+
+def test_work_counted_by_the_bound_on_new_tokens():
+    """4000 requests of a pair of row tiles each over tables of 2^26 rows: by max_seqlen_q their key blocks are below
+    2^31; by the number of rows alone they would not be."""
+    B, n, ps, G = 4000, 64, 1 << 20, 4
+    kc = torch.ones(1, ps, 1, 128, dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros(B, 64, dtype=torch.int32, device="cuda")
+    blocks = 64 * ps // 128 + 4
+    assert B * blocks < 2 ** 31 <= (B * n // (2 * (128 // G)) + B) * blocks
+    q = torch.zeros(B * n, G, 128, dtype=torch.bfloat16, device="cuda")
+    cu = torch.arange(0, B * n + 1, n, dtype=torch.int32, device="cuda")
+    o = b2.attn_paged_fwd(q, kc, kc, table, cu, torch.full((B,), 100, dtype=torch.int32, device="cuda"), max_seqlen_q=n)
+    assert b2.check() == 0 and bool((o == 1).all())
