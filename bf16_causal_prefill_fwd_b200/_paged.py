@@ -45,6 +45,11 @@ def _load():
     if _native is None:
         if not os.path.exists(BINDING_PATH):
             raise RuntimeError(f"{BINDING_PATH} is missing; build it with `python -m bf16_causal_prefill_fwd_b200.build`")
+        from .build import binding_built_for, binding_stamp
+
+        if binding_stamp() not in (None, binding_built_for()):
+            raise RuntimeError(f"{BINDING_PATH} was built for {binding_stamp()}, this is {binding_built_for()}; "
+                               "build it with `python -m bf16_causal_prefill_fwd_b200.build`")
         loader = importlib.machinery.ExtensionFileLoader("_paged_binding", BINDING_PATH)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_paged_binding", loader))
         loader.exec_module(module)

@@ -68,10 +68,27 @@ def _binding_cmd(out: str) -> list[str]:
             "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
 
 
+def binding_built_for() -> str:
+    """What _paged_binding.so is compiled against besides its sources: it uses PyTorch's C++ classes and
+    Python's headers, whose layouts change with their versions. Kept beside it, in _paged_binding.so.stamp."""
+    import torch
+
+    return f"torch {torch.__version__} cxx11abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)} python {sys.version.split()[0]}"
+
+
+def binding_stamp() -> str | None:
+    """What the _paged_binding.so that is there was built for; None if nothing says."""
+    try:
+        with open(BINDING_PATH + ".stamp") as f:
+            return f.read().strip()
+    except OSError:
+        return None
+
+
 def build_binding(force: bool = False) -> str:
-    """Build lib/_paged_binding.so."""
+    """Build lib/_paged_binding.so, if it is older than its sources or built for another PyTorch or Python."""
     src = [os.path.join(CSRC, "paged_binding.cpp"), HEADER]
-    if not force and os.path.exists(BINDING_PATH) and all(
+    if not force and os.path.exists(BINDING_PATH) and binding_stamp() == binding_built_for() and all(
             os.path.getmtime(s) <= os.path.getmtime(BINDING_PATH) for s in src):
         return BINDING_PATH
     os.makedirs(LIB_DIR, exist_ok=True)
@@ -81,6 +98,8 @@ def build_binding(force: bool = False) -> str:
         sys.stderr.write(res.stdout + res.stderr)
         raise RuntimeError("g++ failed building _paged_binding.so")
     os.replace(tmp, BINDING_PATH)
+    with open(BINDING_PATH + ".stamp", "w") as f:
+        f.write(binding_built_for() + "\n")
     return BINDING_PATH
 
 

@@ -271,3 +271,40 @@ def test_the_stated_workspace_is_enough_for_the_call(real, total, max_q, hq):
     assert c_attn(real, c, wsb=need - 1, **args) == -5
     if not torch.cuda.is_available():  # past the checks: no device
         assert c_attn(real, c, wsb=need, **args) == -3
+
+
+# ------------------------------------------------------------------------------------------- the compiled binding
+
+def test_the_binding_is_rebuilt_for_another_torch_or_python(monkeypatch, tmp_path):
+    from bf16_causal_prefill_fwd_b200 import build
+    ran = []
+
+    def compiler(cmd, **kw):
+        ran.append(cmd)
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write("binary")
+        return type("Done", (), {"returncode": 0, "stdout": "", "stderr": ""})
+
+    monkeypatch.setattr(build, "BINDING_PATH", str(tmp_path / "_paged_binding.so"))
+    monkeypatch.setattr(build.subprocess, "run", compiler)
+    for _ in range(2):
+        build.build_binding()
+    assert len(ran) == 1
+    monkeypatch.setattr(torch, "__version__", "0.0")
+    for _ in range(2):
+        build.build_binding()
+    assert len(ran) == 2
+    monkeypatch.setattr(build.sys, "version", "2.7 (old)")
+    build.build_binding()
+    assert len(ran) == 3
+    (tmp_path / "_paged_binding.so.stamp").unlink()   # one that nothing is known of
+    build.build_binding()
+    assert len(ran) == 4
+
+
+def test_a_binding_built_for_another_torch_is_not_loaded(monkeypatch, real):
+    p._load()
+    monkeypatch.setattr(p, "_native", None)
+    monkeypatch.setattr(torch, "__version__", "0.0")
+    with pytest.raises(RuntimeError, match="was built for torch"):
+        p._load()
