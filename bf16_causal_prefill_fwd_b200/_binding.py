@@ -7,6 +7,7 @@ If the library is not built, every call raises: there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -94,6 +95,38 @@ def _stream_handle(stream) -> int | None:
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
+def _tensors(x):
+    return [x] if isinstance(x, torch.Tensor) else [t for y in x for t in _tensors(y)] if isinstance(x, (list, tuple)) else []
+
+
+def _on_stream(fn):
+    """A call that is given ``stream`` runs with it as the current stream, so that what the call allocates belongs to
+    that stream: memory of the caller's current stream could still be in use there when the kernels begin, and a
+    workspace of it would be handed out again when the call returns, under the kernels still running. Results are
+    recorded on the caller's stream too, where they may be read and let go."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        given = _tensors([*args, *kw.values()])
+        if stream is None or not given or not given[0].is_cuda:
+            return fn(*args, stream=stream, **kw)
+        device, handle = given[0].device, _stream_handle(stream)
+        callers = torch.cuda.current_stream(device)
+        if handle in (0, 1):  # 1: cudaStreamLegacy
+            handle, stream = 0, torch.cuda.default_stream(device)
+        elif not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(handle, device=device)
+        if handle == callers.cuda_stream:
+            return fn(*args, stream=stream, **kw)
+        with torch.cuda.stream(stream):
+            r = fn(*args, stream=stream, **kw)
+        for t in _tensors(r):
+            if not any(t is g for g in given):
+                t.record_stream(callers)
+        return r
+
+    return call
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -148,6 +181,7 @@ def _check_scale(name, s, B, H, N, granularity, device):
     _check_buffer(name, s, shape, (torch.float32,), device)
 
 
+@_on_stream
 def attn_fwd(q, k, v, *, causal: bool = True, softmax_scale: float | None = None,
              q_scale=None, k_scale=None, v_scale=None, scale_granularity: str = "head",
              out=None, return_lse: bool = False, stream=None):
@@ -204,6 +238,7 @@ def _cu_device(cu_seqlens, device):
     return torch.tensor(vals, dtype=torch.int32, device=device)
 
 
+@_on_stream
 def attn_varlen_fwd(q, k, v, cu_seqlens, *, causal: bool = True, softmax_scale: float | None = None,
                     q_scale=None, k_scale=None, v_scale=None, out=None, return_lse: bool = False,
                     workspace=None, stream=None):
@@ -258,6 +293,7 @@ def attn_varlen_fwd(q, k, v, cu_seqlens, *, causal: bool = True, softmax_scale: 
     return (out, lse) if return_lse else out
 
 
+@_on_stream
 def attn_varlen_func(q, k, v, cu_seqlens, softmax_scale: float | None = None, causal: bool = True, *,
                      fp8: bool = False, hadamard: bool = False, return_lse: bool = False, stream=None):
     """flash_attn_varlen_func-style call on packed bf16 [total, H, d] tensors (self-attention).
@@ -274,6 +310,7 @@ def quantize_workspace_bytes(B, N, H, d, granularity="head") -> int:
     return int(load_library().b200attn_quantize_workspace_bytes(B, N, H, d, _gran(granularity)))
 
 
+@_on_stream
 def quantize_fp8(x, *, granularity: str = "head", hadamard: bool = False, out=None, scale=None,
                  workspace=None, stream=None):
     """bf16 [B,N,H,d] -> (e4m3 codes as torch.float8_e4m3fn [B,N,H,d], fp32 scales).
@@ -312,6 +349,7 @@ def quantize_qkv_workspace_bytes(B, N, Hq, Hkv, granularity="head") -> int:
     return int(load_library().b200attn_quantize_qkv_workspace_bytes(B, N, Hq, Hkv, _gran(granularity)))
 
 
+@_on_stream
 def quantize_qkv_fp8(q, k, v, *, granularity: str = "head", hadamard: bool = False, out=None, workspace=None,
                      stream=None):
     """bf16 Q, K, V -> (q8, sq, k8, sk, v8, sv) through b200attn_quantize_qkv_fp8: one
@@ -360,6 +398,7 @@ def quantize_kv_workspace_bytes(B, N, Hkv, granularity="head") -> int:
     return int(load_library().b200attn_quantize_kv_workspace_bytes(B, N, Hkv, _gran(granularity)))
 
 
+@_on_stream
 def quantize_kv_fp8(k, v, *, granularity: str = "head", hadamard: bool = False, out=None, workspace=None,
                     stream=None):
     """bf16 K, V -> (k8, sk, v8, sv) through b200attn_quantize_kv_fp8 (the rotation,
@@ -404,6 +443,7 @@ def quantize_kv_fp8(k, v, *, granularity: str = "head", hadamard: bool = False, 
     return k8, sk, v8, sv
 
 
+@_on_stream
 def attn_fwd_fused_q(q, k8, v8, *, k_scale, v_scale, causal: bool = True, softmax_scale: float | None = None,
                      hadamard: bool = False, out=None, return_lse: bool = False, q_out=None, q_scale_out=None,
                      stream=None):
@@ -446,6 +486,7 @@ def attn_fwd_fused_q(q, k8, v8, *, k_scale, v_scale, causal: bool = True, softma
     return (out, lse) if return_lse else out
 
 
+@_on_stream
 def attn_func(q, k, v, softmax_scale: float | None = None, causal: bool = True, *, fp8: bool = False,
               hadamard: bool = False, granularity: str = "q_block", fused_q: bool = False, return_lse: bool = False,
               stream=None):
