@@ -115,11 +115,12 @@ def attn_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, *, max
 
 
 def attn_paged_func(q, k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, slots, softmax_scale: float | None = None,
-                    causal: bool = True, *, max_seqlen_q: int | None = None, k_scale=None, v_scale=None,
-                    return_lse: bool = False, stream=None):
+                    causal: bool = True, *, max_seqlen_q: int | None = None, k_scale=None, v_scale=None, out=None,
+                    return_lse: bool = False, workspace=None, stream=None):
     """One layer's attention of a serving step: paged_append_kv of the new K and V rows, then attn_paged_fwd of the
-    new queries over the pages (cu_seqlens, kv_lens and slots as paged_slots gives them)."""
+    new queries over the pages (cu_seqlens, kv_lens and slots as paged_slots gives them; out and workspace as
+    attn_paged_fwd takes them)."""
     paged_append_kv(k, v, k_cache, v_cache, slots, k_scale=k_scale, v_scale=v_scale, stream=stream)
     return attn_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, max_seqlen_q=max_seqlen_q,
-                          causal=causal, softmax_scale=softmax_scale, k_scale=k_scale, v_scale=v_scale,
-                          return_lse=return_lse, stream=stream)
+                          causal=causal, softmax_scale=softmax_scale, k_scale=k_scale, v_scale=v_scale, out=out,
+                          return_lse=return_lse, workspace=workspace, stream=stream)

@@ -116,6 +116,15 @@ def test_views_the_kernels_take_as_they_are(lib):
     assert strides == (PS * HKV * D, D, PS * D, 2 * PS * HKV * D, HKV * D, D)
 
 
+def test_one_layers_call_takes_the_buffers_of_its_halves(lib):
+    """What a captured step has to keep alive can be given to attn_paged_func as to attn_paged_fwd."""
+    out, ws = bf16(T, HQ, D), torch.zeros(64, dtype=torch.uint8)
+    got = p.attn_paged_func(bf16(T, HQ, D), bf16(T, HKV, D), bf16(T, HKV, D), bf16(P, PS, HKV, D), bf16(P, PS, HKV, D),
+                            ints(B, W), ints(B + 1), ints(B), ints(T), max_seqlen_q=2, out=out, workspace=ws, stream=0)
+    assert got is out and [name for name, _ in lib.calls] == ["append", "fwd"]
+    assert lib.calls[1][1][14] == out.data_ptr() and lib.calls[1][1][16:18] == [ws.data_ptr(), 64]
+
+
 def test_no_new_tokens_is_no_work(lib):
     o = attn(lib, q=bf16(0, HQ, D))
     assert o.shape == (0, HQ, D) and lib.calls == []
