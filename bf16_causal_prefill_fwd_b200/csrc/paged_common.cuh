@@ -104,6 +104,13 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t c) {
   return r;
 }
 
+// Two fp32 -> f16x2, lo in bits [0,16), held at +-65504; NaN stays NaN.
+__device__ __forceinline__ uint32_t pack_f16x2_sat(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 __device__ __forceinline__ float fast_log2(float x) {
   float y;
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));

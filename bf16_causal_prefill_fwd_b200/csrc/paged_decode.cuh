@@ -412,12 +412,12 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<DQK, DV, FP8, NT>::BLOCKS)
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            if constexpr (FP8) mx -= kHalfExp;
             const float mn = fmaxf(m[j][i], mx);
             alpha[j][i] = mn > m[j][i] ? ex2_approx(m[j][i] - mn) : 1.0f;
             moved |= mn > m[j][i];
             m[j][i] = mn;
-            // nothing seen yet: every probability is 0
-            const float ref = (mn == -INFINITY ? 0.0f : mn) - (FP8 ? kHalfExp : 0.0f);
+            const float ref = mn == -INFINITY ? 0.0f : mn;  // nothing seen yet: every probability is 0
             float sum = 0.0f;
 #pragma unroll
             for (int gi = 0; gi < C::KG; ++gi) {
@@ -429,8 +429,9 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<DQK, DV, FP8, NT>::BLOCKS)
           }
 #pragma unroll
           for (int gi = 0; gi < C::KG; ++gi) {
-            pb[gi][j][0] = movm_t(FP8 ? pack_f16x2(x[gi][0], x[gi][1]) : pack_bf16x2(x[gi][0], x[gi][1]));
-            pb[gi][j][1] = movm_t(FP8 ? pack_f16x2(x[gi][2], x[gi][3]) : pack_bf16x2(x[gi][2], x[gi][3]));
+            // (held at fp16's largest: where scores above 2^24 are rounded, m - 15 may be m - 16)
+            pb[gi][j][0] = movm_t(FP8 ? pack_f16x2_sat(x[gi][0], x[gi][1]) : pack_bf16x2(x[gi][0], x[gi][1]));
+            pb[gi][j][1] = movm_t(FP8 ? pack_f16x2_sat(x[gi][2], x[gi][3]) : pack_bf16x2(x[gi][2], x[gi][3]));
           }
         }
         if (__any_sync(0xffffffffu, moved)) {
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<DQK, DV, FP8, NT>::BLOCKS)
         if (lane < 4) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            s_ml[(warp * 8 + 2 * lane + i) * 2] = m[j][i] - (FP8 ? kHalfExp : 0.0f);
+            s_ml[(warp * 8 + 2 * lane + i) * 2] = m[j][i];
             s_ml[(warp * 8 + 2 * lane + i) * 2 + 1] = l[j][i];
           }
         }

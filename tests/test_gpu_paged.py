@@ -634,6 +634,34 @@ def test_long_contexts_with_a_rising_maximum(n_new, kv, e4m3):
         assert bool(((got_lse[h].double().cpu() - lse).abs() <= score[:, 0] + 2.0 ** -22 * (2 + lse.abs()) + kv / 64 * 2.0 ** -24).all())
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n_new,kv", [(1, 3000), (2, 700), (40, 3000)])
+@pytest.mark.parametrize("power", [14, 16, 17, 18, 19])
+def test_very_large_scores_give_the_largest_ones_value(n_new, kv, e4m3, power):
+    """Scores of up to 2^25 binades, where fp32 numbers are 0.125 to 4 apart: rows whose largest score stands out by more
+    than its rounding give that key's value."""
+    p = make([n_new], [kv], 8, 2, 128, 16, e4m3, seed=80 + power)
+    scale = 2.0 ** power
+    o, _ = run(p, max_seqlen_q=n_new, softmax_scale=scale)
+    want, _, _, reach = attention(p, softmax_scale=scale)
+    row = p.table[0].long()
+    j = torch.arange(kv)
+    hits = 0
+    for h in range(8):
+        k, v = (c[row[j // 16], j % 16, h // 4].double() for c in (p.k_cache, p.v_cache))
+        if e4m3:
+            k, v = k * p.k_scale[h // 4].double(), v * p.v_scale[h // 4].double()
+        x = p.q[:, h].double() @ k.T * scale
+        x[j[None, :] > kv - n_new + torch.arange(n_new)[:, None]] = -math.inf
+        top, at = x.topk(2, 1)
+        clear = top[:, 0] - top[:, 1] > 40 + 2 * (128 + 2) * 2.0 ** -24 * reach[h]  # the score's error, see check_attention
+        hits += int(clear.sum())
+        # one half step of the probability's type and one of the output's
+        lim = v[at[:, 0]].abs() * (2.0 ** -8 + (2.0 ** -11 if e4m3 else 2.0 ** -8)) + 1e-9
+        assert bool(((o[:, h].double().cpu() - v[at[:, 0]]).abs() <= lim)[clear].all())
+    assert hits >= 4 * n_new and not bool(o.isnan().any())
+
+
 # ------------------------------------------------------------------------------------------- as a server uses them
 
 def dense(q, k, v, n_ctx):
