@@ -4,7 +4,8 @@ A cache is two tensors, k_cache [pages, page_size, Hkv, d_qk] and v_cache
 [pages, page_size, Hkv, d_v], bf16 or e4m3 (torch.float8_e4m3fn or uint8 codes)
 with one positive fp32 scale per key/value head. They may be views (a [pages, Hkv,
 page_size, d] buffer permuted, K and V halves of one buffer): rows of d elements
-are contiguous, the other strides are multiples of 16 bytes.
+are contiguous, the other strides are multiples of 16 bytes. page_size is a multiple
+of 16 (any for paged_slots alone).
 
 Lengths, tables and slots are int32 CUDA tensors read on the device only: no call
 here copies from the device or waits for it, so each can be captured into a CUDA
@@ -70,7 +71,8 @@ def paged_slots(block_table, context_lens, new_lens, total: int, page_size: int,
     ``total`` is the number of token rows the step is run with; rows behind the last new token get slot -1. With
     ``free_pages`` (int32 page numbers) the pages the new tokens need are taken from entry free_head[0] on and
     written into block_table, and a fifth result holds the new head (``free_head_out``, which may be free_head
-    itself, or a new tensor). A step that does not fit is empty, and check() says why: -1 for lengths that do not
+    itself, or a new tensor). Results that are not given are parts of one allocation, each contiguous, which lives
+    as long as any of them. A step that does not fit is empty, and check() says why: -1 for lengths that do not
     fit, -6 for too few free pages.
     """
     r = (_native or _load()).slots(block_table, context_lens, new_lens, total, page_size, free_pages, free_head,

@@ -191,9 +191,9 @@ Parts parts_of(int blocks, int rows) {
 
 // The few-rows kernel serves up to 16 query rows per key/value head; the choice
 // is by the bound on a request's new tokens alone, which the host knows. At 16 rows
-// (4 tokens, 4 heads a group) 64 requests over up to 16k bf16 keys take 323 us with
-// it and 377 with the other, one over 4096 16.4 and 21.1; 24 requests of 12 rows over
-// 9-32k e4m3 keys 199 and 329. Above, its rows would no longer fit the registers.
+// (4 tokens, 4 heads a group) 64 requests over up to 16k bf16 keys take 313-354 us with
+// it and 314-369 with the other, one over 4096 17-23 and 20-27; 24 requests of 12 rows
+// over 9-32k e4m3 keys 187 and 307. Above, its rows would no longer fit the registers.
 bool few_rows(int max_q, int G) { return static_cast<int64_t>(max_q) * G <= b200p::kDecMaxRows; }
 
 template <int DQK, bool FP8, int NT>
@@ -358,8 +358,8 @@ int b200attn_paged_append(const void* k, const void* v, size_t k_stride, size_t 
   p.page_size = b200p::fast_div(cache->page_size);
   p.per_token = b200p::fast_div(cache->Hkv * ((cache->d_qk + cache->d_v) / b200p::kAppendUnit));
   const int64_t want = (units + b200p::kAppendThreads - 1) / b200p::kAppendThreads;
-  // One unit per thread while the grid is below 64 blocks per SM: measured on 16k tokens, 8 blocks per SM looping
-  // take 23.6 us (bf16) and 20.7 us (e4m3), 64 take 20.7 and 19.4; two or four units in flight per thread were slower.
+  // One unit per thread while the grid is below 64 blocks per SM: measured side by side on 16k tokens, 8 blocks per SM
+  // looping took 23.6 us (bf16) and 20.7 us (e4m3), 64 20.7 and 19.4; two or four units in flight per thread were slower.
   const int blocks = static_cast<int>(want < 64 * sm_count ? want : 64 * sm_count);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   auto kern = cache->dtype == B200ATTN_BF16

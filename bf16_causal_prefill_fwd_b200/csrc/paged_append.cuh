@@ -9,8 +9,8 @@
 // half of that written. A thread moves units of 16 elements (two 16-byte loads,
 // one or two 16-byte stores) of K and V alike; consecutive threads take
 // consecutive units of a token's row, so loads and stores are whole lines
-// whatever the order of the slots. 16384 tokens of 8 heads of 128: bf16 21.6 us
-// (6.05 TB/s), e4m3 18.3-19.0 us (5.2 TB/s; the conversion's instructions take 78% of
+// whatever the order of the slots. 16384 tokens of 8 heads of 128: bf16 20.7-22.4 us
+// (6.0-6.5 TB/s), e4m3 18.4-18.9 us (5.3 TB/s; the conversion's instructions take 78% of
 // the issue slots with one element at a time, 21.2 us, which is why it works on pairs).
 #pragma once
 

@@ -37,13 +37,19 @@
 // is fp16. Converting K as well, with four more warps, took 503 us where this
 // took 395 then (4 requests of 500-1300 new tokens, 2-12k keys).
 //
+// P is rounded to 16 bits for the second product (bf16, or fp16 as ch_p_exp says) and
+// summed in fp32 as it was: both operands of a product have one type, and a second
+// part of P would be half as many products again. With bf16 the result is 0.0023 of its
+// size (rms) off the one in 64 bits, its own rounding alone 0.0017, each the same half
+// step; with fp16 0.0017.
+//
 // Bound by the tensor core (2 x 2 x 128^3 products per key block and pair) and,
-// for chunks of a few tokens, by reading the cache. Measured: 4096 tokens over 32k
-// keys (32/8 heads of 128, bf16) 1.65-1.69 ms, 1220-1250 TFLOP/s under the power cap,
-// tensor pipe 77% busy, MUFU 80%; ragged chunks of 1-1500 tokens 168-187 us (55%: each
+// for chunks of a few tokens, by reading the cache. Measured, a call: 4096 tokens over
+// 32k keys (32/8 heads of 128, bf16) 1.65-1.72 ms, 1200-1250 TFLOP/s under the power cap,
+// tensor pipe 79% busy, MUFU 80%; ragged chunks of 1-1500 tokens 183-188 us (53%: each
 // SM's run begins with an empty pipeline and ends with a part to write and join); the
-// same kind over an e4m3 cache 351-363 us (51%); 192/128 heads 214-249 us (58%); 32
-// requests of 3-9 drafted tokens 117-135 us, 4.8-5.5 TB/s of cache.
+// same kind over an e4m3 cache 344-353 us (52%); 192/128 heads 246-250 us (57%), e4m3
+// 215-221 us; 32 requests of 3-9 drafted tokens 128-134 us, 4.8-5.0 TB/s of cache.
 #pragma once
 
 #include "paged_common.cuh"
@@ -131,7 +137,8 @@ __device__ __forceinline__ int shift_sum(int x, int k) {
 
 // sum of floor((a i + b) / m) over i = 0 .. n - 1 (a, b >= 0; m = kChN, a power of
 // two): in closed form if a is one too, else by exchanging the roles of a and m as
-// in Euclid's algorithm: a few steps, whatever n.
+// in Euclid's algorithm: a few steps, whatever n (such sums and their reciprocity:
+// Graham, Knuth and Patashnik, "Concrete Mathematics", 1989, section 3.5).
 __device__ __forceinline__ int floor_sum(int n, int m, int a, int b) {
   int s = 0;
   if ((a & (a - 1)) == 0) {

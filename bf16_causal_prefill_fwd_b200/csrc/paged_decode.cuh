@@ -27,15 +27,21 @@
 // concern here: 16 products per 8 KB of cache.
 //
 // Measured (G = 4, Hkv = 8, d = 128): 64 requests of up to 16k keys, bf16, 1.88 GB
-// of cache: 280 us, 6.7 TB/s, what a plain copy reaches; 24 requests of 9-32k keys,
-// e4m3, 1.0 GB: 170 us, 5.9 TB/s, held back by the conversions (30% of the issue
-// slots in bursts between the products); one request of 4096 keys: 9.1 us, of which
-// two launches and the join are about 6.
+// of cache: 278-290 us, 6.5-6.75 TB/s, what a plain copy reaches; 24 requests of 9-32k
+// keys, e4m3, 1.0 GB: 168-176 us, 5.65-5.95 TB/s, held back by the conversions (31% of the
+// issue slots in bursts between the products); one request of 4096 keys: 9.1 us, of
+// which two launches and the join are about 6. 16 heads of 192/128, 32 requests of
+// 1-16k keys: bf16 462-474 us (6.8-7.0 TB/s), e4m3 282-298 us (5.4-5.7 TB/s). 12 rows of
+// 24 requests, e4m3: 182-187 us.
 //
 // e4m3 caches: codes become fp16 exactly (cvt.rn.f16x2.e4m3x2), Q is brought to
 // fp16 by a power of two per row (its largest element in [1/2, 1): every bf16
 // above 2^-16 of it keeps all its bits), P is fp16; the scales of K and V go
-// into the softmax factor and the output.
+// into the softmax factor and the output. The probabilities are rounded to 16 bits
+// for the second product (bf16, or fp16 as kHalfExp says) and summed as they were:
+// the product's operands have one type, and a second part of P would double it. A
+// row's largest is exactly 1 here, so the result is hardly further from 64 bits (0.0018
+// of its size rms, bf16) than its own rounding (0.0017).
 #pragma once
 
 #include "paged_common.cuh"
@@ -44,7 +50,8 @@ namespace b200p {
 
 constexpr int kDecWarps = 4;     // consumer warps
 // Keys per tile (one stage of the ring): 16 per warp, of an e4m3 cache 32, whose
-// two groups' conversions and products fill each other's gaps.
+// two groups' conversions and products fill each other's gaps (24 requests of 9-32k
+// keys 182 -> 170 us). At 192 two stages of that size would not fit two blocks an SM.
 __host__ __device__ constexpr int dec_keys(bool fp8, int d_qk) { return fp8 && d_qk == 128 ? 128 : 64; }
 constexpr int kDecThreads = 32 * (kDecWarps + 1);
 constexpr int kDecMaxBlocks = 480;  // workspace slots are sized for this many blocks
@@ -64,7 +71,9 @@ struct DecCfg {
   static constexpr int ML = kDecWarps * 8 * 2 * 4;      // their (m, l)
   static constexpr int FIXED = MERGE + ML + 512 /*barriers, plan*/ + 1024 /*alignment*/;
   // Blocks per SM. Two are enough to stream bf16 pages; with e4m3 a tile is half
-  // the bytes for more instructions, and a third block's warps fill the gaps.
+  // the bytes for more instructions, and where a warp has 16 keys of it (192/128) a
+  // third block's warps fill the gaps: 32 requests of 1-16k keys 283 us for 284.6 with
+  // two, 4 of 1-8k 20.8 for 21.4, 24 of 4-16k with 32/8 heads 112.0 for 113.5.
   static constexpr int BLOCKS = FP8 && NT == 1 && KG == 1 ? 3 : 2;
   static constexpr int BUDGET = 227 * 1024 / BLOCKS / 1024 * 1024 - (BLOCKS == 2 ? 0 : 1024);
   static constexpr int FIT = (BUDGET - FIXED) / STAGE;
