@@ -873,8 +873,9 @@ __global__ void __launch_bounds__(ChCfg<DQK, DV, FP8>::THREADS, 1)
         x1 = max3_nan(x1, __uint_as_float(sr[126]), __uint_as_float(sr[127]));
         x0 = max3_nan(x0, x1, x2);
         const float m_new = max2_nan(x0 * c_log2, x3 * c_log2);
-        // fp16: large scores, whose rounding is more than a fraction of a binade, leave that much less room
-        const float room = FP8 ? fmaf(fabsf(m_ref), -0x1p-22f, C::P_MAX) : C::P_MAX;
+        // fp16: large scores, whose rounding is more than a fraction of a binade, leave that much less room (the
+        // reference itself never moves down)
+        const float room = FP8 ? fmaxf(fmaf(fabsf(m_ref), -0x1p-22f, C::P_MAX), p_exp) : C::P_MAX;
         const bool need = !(m_new <= m_ref + room);  // true for NaN too
         float alpha = 1.0f;
         if (need) {

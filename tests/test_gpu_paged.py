@@ -662,6 +662,25 @@ def test_very_large_scores_give_the_largest_ones_value(n_new, kv, e4m3, power):
     assert hits >= 4 * n_new and not bool(o.isnan().any())
 
 
+def test_falling_maxima_of_very_large_scores():
+    """Scores of 2^26.9 binades that fall by one or two steps of fp32 a key block: the first block's keys have all the
+    weight, and what has been summed up is not scaled up block by block. As many requests as SMs, so that none is split."""
+    n, blocks, B = 40, 10, torch.cuda.get_device_properties(0).multi_processor_count
+    k, v = torch.zeros(blocks * 8, 16, 1, 128), torch.full((blocks * 8, 16, 1, 128), -1.0)
+    k[..., 0], v[:8] = 256.0, 1.0
+    k[..., 1] = torch.arange(blocks - 1, -1, -1).repeat_interleave(8)[:, None, None]
+    q = torch.zeros(B * n, 4, 128, dtype=torch.bfloat16, device="cuda")
+    q[..., 0], q[..., 1] = 1.0, 2.0 ** -15
+    one = torch.ones(1, device="cuda")
+    o = b2.attn_paged_fwd(q, *(x.to(torch.float8_e4m3fn).cuda() for x in (k, v)),
+                          torch.arange(blocks * 8, dtype=torch.int32, device="cuda").repeat(B, 1),
+                          ints([n * i for i in range(B + 1)]), ints([blocks * 128] * B), max_seqlen_q=n, causal=False,
+                          softmax_scale=2.0 ** 26.9 / 256 / math.log2(math.e), k_scale=one, v_scale=one)
+    assert b2.check() == 0
+    # the blocks behind the first have 2^-8 of its weight each at most, as far apart as fp32 numbers of this size are
+    assert bool(((o.float() - 1).abs() <= 2 * 2.0 ** -7 + 2.0 ** -8).all())
+
+
 # ------------------------------------------------------------------------------------------- as a server uses them
 
 def dense(q, k, v, n_ctx):
